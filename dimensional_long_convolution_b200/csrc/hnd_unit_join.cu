@@ -1,0 +1,296 @@
+// The residual join with the norms on both sides of it, forward and backward.
+#include "hnd_block.h"
+#include "hnd_io.cuh"
+#include "hnd_philox.cuh"
+
+namespace hnd {
+
+constexpr int kJoinLanes = 32;   // positions of a block
+constexpr int kJoinRows = 8;     // channel rows of a block
+
+// Everything a kernel needs of a join, by value.
+struct JoinDev {
+  long long B, C, L, T;
+  int post, pre;
+  float eps1, eps2;
+  const float *w1, *b1, *w2, *b2, *gate, *scale;
+  unsigned border;
+  float factor;
+  const int64_t* rng;
+};
+
+// One position's view of the join: values at channel c.
+template <class TT>
+struct Pos {
+  const JoinDev& j;
+  const TT *x, *y;
+  long long b, base;      // sample, index of channel 0 in [B, C, L]
+  DropState ds;
+  float mu1 = 0.f, rho1 = 1.f, mu2 = 0.f, rho2 = 1.f;
+
+  __device__ Pos(const JoinDev& jj, const TT* xx, const TT* yy, long long t) : j(jj), x(xx), y(yy), ds{} {
+    b = t / j.L;
+    base = b * j.C * j.L + t % j.L;
+    if (j.border) ds = drop_state(j.rng);
+  }
+  __device__ long long at(long long c) const { return base + c * j.L; }
+  __device__ float yhat(long long c) const { return (ld1(y + at(c)) - mu1) * rho1; }
+  __device__ float w1(long long c) const { return j.w1 ? ld1(j.w1 + c) : 1.f; }
+  __device__ float w2(long long c) const { return j.w2 ? ld1(j.w2 + c) : 1.f; }
+  __device__ float m(long long c) const {
+    if (!j.border) return 1.f;
+    const long long i = at(c);
+    return drop_lot(drop_lots(ds, static_cast<uint64_t>(i >> 3)), static_cast<int>(i & 7)) >= j.border ? j.factor
+                                                                                                       : 0.f;
+  }
+  __device__ float sg(long long c) const {
+    return (j.scale ? ld1(j.scale + c) : 1.f) * (j.gate ? ld1(j.gate + b * j.C + c) : 1.f);
+  }
+  __device__ float h(long long c) const {
+    const float xv = ld1(x + at(c));
+    if (!y) return xv;
+    const float f = m(c);
+    if (f == 0.f) return xv;
+    const float z = yhat(c) * w1(c) + (j.b1 ? ld1(j.b1 + c) : 0.f);
+    return xv + sg(c) * (f * z);
+  }
+  __device__ float hhat(long long c) const { return (h(c) - mu2) * rho2; }
+};
+
+// Sum over the channel rows of a block, for each of its positions.
+__device__ __forceinline__ float rows_sum(float v, float (*buf)[kJoinLanes]) {
+  __syncthreads();
+  buf[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) s += buf[r][threadIdx.x];
+  return s;
+}
+
+// Mean and reciprocal deviation of f(c) over the channels.
+template <class Fn>
+__device__ __forceinline__ void norm_stats(int kind, float eps, long long C, bool live, float (*buf)[kJoinLanes],
+                                           float& mu, float& rho, Fn f) {
+  mu = 0.f;
+  rho = 1.f;
+  if (!kind) return;
+  const float inv = 1.f / static_cast<float>(C);
+  if (kind == 2) {
+    float s = 0.f;
+    if (live)
+      for (long long c = threadIdx.y; c < C; c += kJoinRows) s += f(c);
+    mu = rows_sum(s, buf) * inv;
+  }
+  float s = 0.f;
+  if (live)
+    for (long long c = threadIdx.y; c < C; c += kJoinRows) {
+      const float d = f(c) - mu;
+      s += d * d;
+    }
+  rho = rsqrtf(rows_sum(s, buf) * inv + eps);
+}
+
+template <class TT>
+__device__ __forceinline__ void pos_stats(Pos<TT>& p, bool live, float (*buf)[kJoinLanes]) {
+  const JoinDev& j = p.j;
+  if (p.y) {
+    float mu, rho;
+    norm_stats(j.post, j.eps1, j.C, live, buf, mu, rho, [&](long long c) { return ld1(p.y + p.at(c)); });
+    p.mu1 = mu;
+    p.rho1 = rho;
+  }
+  float mu, rho;
+  norm_stats(j.pre, j.eps2, j.C, live, buf, mu, rho, [&](long long c) { return p.h(c); });
+  p.mu2 = mu;
+  p.rho2 = rho;
+}
+
+template <class TT>
+__global__ void __launch_bounds__(kJoinLanes* kJoinRows)
+    k_join_fwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, TT* __restrict__ h, TT* __restrict__ n) {
+  __shared__ float buf[kJoinRows][kJoinLanes];
+  const long long t = blockIdx.x * static_cast<long long>(kJoinLanes) + threadIdx.x;
+  const bool live = t < j.T;
+  Pos<TT> p(j, x, y, live ? t : 0);
+  pos_stats(p, live, buf);
+  if (!live) return;
+  for (long long c = threadIdx.y; c < j.C; c += kJoinRows) {
+    const float hv = p.h(c);
+    if (h) st1(h + p.at(c), hv);
+    if (n) st1(n + p.at(c), (hv - p.mu2) * p.rho2 * p.w2(c) + (j.b2 ? ld1(j.b2 + c) : 0.f));
+  }
+}
+
+// Statistics of a position that the parameter gradients need again.
+struct JoinStat {
+  float mu1, rho1, mu2, rho2, s1, s2, pad0, pad1;
+};
+
+template <class TT>
+__device__ __forceinline__ float whole_grad(const Pos<TT>& p, const TT* dh, const TT* dn, long long c, float s1,
+                                            float s2) {
+  float d = dh ? ld1(dh + p.at(c)) : 0.f;
+  if (dn) d += p.rho2 * (ld1(dn + p.at(c)) * p.w2(c) - s1 - p.hhat(c) * s2);
+  return d;
+}
+
+template <class TT>
+__global__ void __launch_bounds__(kJoinLanes* kJoinRows)
+    k_join_bwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
+               const TT* __restrict__ dn, TT* __restrict__ dx, TT* __restrict__ dy, JoinStat* __restrict__ stats) {
+  __shared__ float buf[kJoinRows][kJoinLanes];
+  const long long t = blockIdx.x * static_cast<long long>(kJoinLanes) + threadIdx.x;
+  const bool live = t < j.T;
+  Pos<TT> p(j, x, y, live ? t : 0);
+  pos_stats(p, live, buf);
+  const float inv = 1.f / static_cast<float>(j.C);
+  float s1 = 0.f, s2 = 0.f;
+  if (dn && live)
+    for (long long c = threadIdx.y; c < j.C; c += kJoinRows) {
+      const float a = ld1(dn + p.at(c)) * p.w2(c);
+      s1 += a;
+      s2 += a * p.hhat(c);
+    }
+  s1 = j.pre == 2 ? rows_sum(s1, buf) * inv : 0.f;
+  s2 = rows_sum(s2, buf) * inv;
+  float s3 = 0.f, s4 = 0.f;
+  if (y && j.post) {
+    if (live)
+      for (long long c = threadIdx.y; c < j.C; c += kJoinRows) {
+        const float f = p.m(c);
+        if (f == 0.f) continue;
+        const float e = whole_grad(p, dh, dn, c, s1, s2) * f * p.sg(c) * p.w1(c);
+        s3 += e;
+        s4 += e * p.yhat(c);
+      }
+    s3 = j.post == 2 ? rows_sum(s3, buf) * inv : 0.f;
+    s4 = rows_sum(s4, buf) * inv;
+  }
+  if (!live) return;
+  for (long long c = threadIdx.y; c < j.C; c += kJoinRows) {
+    const float d = whole_grad(p, dh, dn, c, s1, s2);
+    st1(dx + p.at(c), d);
+    if (y) {
+      const float f = p.m(c);
+      const float e = f == 0.f ? 0.f : d * f * p.sg(c) * p.w1(c);
+      st1(dy + p.at(c), j.post ? p.rho1 * (e - s3 - p.yhat(c) * s4) : e);
+    }
+  }
+  if (threadIdx.y == 0) *HND_G(stats + t) = JoinStat{p.mu1, p.rho1, p.mu2, p.rho2, s1, s2, 0.f, 0.f};
+}
+
+// Per (b, c): sums over the positions of dht m yhat, dht m, dn hhat, dn.
+template <class TT>
+__global__ void __launch_bounds__(256)
+    k_join_param(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
+                 const TT* __restrict__ dn, const JoinStat* __restrict__ stats, float4* __restrict__ part) {
+  const long long bc = blockIdx.x, b = bc / j.C, c = bc % j.C;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (long long l = threadIdx.x; l < j.L; l += 256) {
+    const long long t = b * j.L + l;
+    Pos<TT> p(j, x, y, t);
+    const JoinStat st = *HND_G(stats + t);
+    p.mu1 = st.mu1, p.rho1 = st.rho1, p.mu2 = st.mu2, p.rho2 = st.rho2;
+    if (y) {
+      const float f = p.m(c);
+      if (f != 0.f) {
+        const float d = whole_grad(p, dh, dn, c, st.s1, st.s2) * f;
+        s.x += d * p.yhat(c);
+        s.y += d;
+      }
+    }
+    if (dn) {
+      const float v = ld1(dn + p.at(c));
+      s.z += v * p.hhat(c);
+      s.w += v;
+    }
+  }
+  __shared__ float4 buf[256];
+  buf[threadIdx.x] = s;
+  __syncthreads();
+  for (int k = 128; k > 0; k /= 2) {
+    if (threadIdx.x < k) {
+      float4 &u = buf[threadIdx.x], v = buf[threadIdx.x + k];
+      u.x += v.x, u.y += v.y, u.z += v.z, u.w += v.w;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *HND_G(part + bc) = buf[0];
+}
+
+struct JoinGradsDev {
+  float *w1, *b1, *gate, *scale, *w2, *b2;
+};
+
+__global__ void __launch_bounds__(256) k_join_grads(JoinDev j, const float4* __restrict__ part, JoinGradsDev g) {
+  const long long c = blockIdx.x * 256LL + threadIdx.x;
+  if (c >= j.C) return;
+  const float w1 = j.w1 ? ld1(j.w1 + c) : 1.f, b1 = j.b1 ? ld1(j.b1 + c) : 0.f;
+  const float sc = j.scale ? ld1(j.scale + c) : 1.f;
+  float dw1 = 0.f, db1 = 0.f, ds = 0.f, dw2 = 0.f, db2 = 0.f;
+  for (long long b = 0; b < j.B; ++b) {
+    const float4 s = *HND_G(part + b * j.C + c);
+    const float gt = j.gate ? ld1(j.gate + b * j.C + c) : 1.f;
+    const float z = w1 * s.x + b1 * s.y;
+    if (g.gate) st1(g.gate + b * j.C + c, sc * z);
+    dw1 += sc * gt * s.x;
+    db1 += sc * gt * s.y;
+    ds += gt * z;
+    dw2 += s.z;
+    db2 += s.w;
+  }
+  if (g.w1) st1(g.w1 + c, dw1);
+  if (g.b1) st1(g.b1 + c, db1);
+  if (g.scale) st1(g.scale + c, ds);
+  if (g.w2) st1(g.w2 + c, dw2);
+  if (g.b2) st1(g.b2 + c, db2);
+}
+
+static JoinDev device_view(const JoinArgs& a) {
+  return {a.B,      a.C,      a.L,    a.B * a.L, a.post.kind, a.pre.kind,    a.post.eps,    a.pre.eps, a.post.w,
+          a.post.b, a.pre.w,  a.pre.b, a.gate,    a.scale,     a.drop.border, a.drop.factor, a.drop.rng};
+}
+
+template <class TT>
+static cudaError_t forward(const JoinArgs& a) {
+  const JoinDev j = device_view(a);
+  const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
+  k_join_fwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(
+      j, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h), static_cast<TT*>(a.n));
+  return cudaGetLastError();
+}
+
+static size_t stats_bytes(long long T) { return (static_cast<size_t>(T) * sizeof(JoinStat) + 255) / 256 * 256; }
+
+size_t join_workspace(long long B, long long C, long long L) {
+  return stats_bytes(B * L) + static_cast<size_t>(B * C) * sizeof(float4);
+}
+
+template <class TT>
+static cudaError_t backward(const JoinArgs& a) {
+  const JoinDev j = device_view(a);
+  const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
+  JoinStat* stats = static_cast<JoinStat*>(a.ws);
+  float4* part = reinterpret_cast<float4*>(static_cast<char*>(a.ws) + stats_bytes(j.T));
+  const TT *x = static_cast<const TT*>(a.x), *y = static_cast<const TT*>(a.y), *dh = static_cast<const TT*>(a.dh),
+           *dn = static_cast<const TT*>(a.dn);
+  k_join_bwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(j, x, y, dh, dn, static_cast<TT*>(a.dx),
+                                                                      static_cast<TT*>(a.dy), stats);
+  if (a.dpost_w || a.dpost_b || a.dgate || a.dscale || a.dpre_w || a.dpre_b) {
+    k_join_param<TT><<<static_cast<unsigned>(j.B * j.C), 256, 0, a.stream>>>(j, x, y, dh, dn, stats, part);
+    k_join_grads<<<static_cast<unsigned>((j.C + 255) / 256), 256, 0, a.stream>>>(
+        j, part, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_join_forward(const JoinArgs& a) {
+  return a.bf16 ? forward<__nv_bfloat16>(a) : forward<float>(a);
+}
+
+cudaError_t launch_join_backward(const JoinArgs& a) {
+  return a.bf16 ? backward<__nv_bfloat16>(a) : backward<float>(a);
+}
+
+}  // namespace hnd

@@ -1,0 +1,678 @@
+// hnd_ffn_gemm.cuh -- the matrix products of the gated feed-forward block on
+// the fifth-generation tensor cores, with the block's activation in their
+// epilogues.
+//
+// Every product is D[n][m] = sum_k A(m, k) B(k, n) with m along the
+// contiguous axis of D: m runs over positions (or, for weight gradients, over
+// a weight's contiguous channels) and lies in the lanes of tensor memory, so
+// that a warp's stores of one n are adjacent.  Operands keep the layout they
+// have in memory: a tile whose m (or n) axis is the contiguous one is staged
+// "MN-major", otherwise "K-major"; both in 128-byte swizzled shared memory,
+// brought by TMA, whose out-of-range zeros cover every ragged edge.
+//
+// A pair of CTAs computes a 256 x 256 tile (cta_group::2): each holds 128 rows
+// of A, half of B's columns and 128 accumulator lanes.  One warp issues TMA,
+// one (of the leading CTA) the MMAs, eight read the accumulators back.
+// Accumulators are fp32 in tensor memory, two of 256 columns, so that the
+// epilogue of a tile runs under the products of the next (three of 128
+// columns, once, where the epilogue needs G, U and dH together).
+//
+// fp32 operands come as three bf16 planes (high, middle, low: 24 bits) and
+// every K loop runs over the six plane products that reach 2^-24, the small
+// ones first.  The tensor core truncates where it adds to an accumulator, a
+// loss that grows with the number of additions (measured: 1.0e-6 of the
+// result at depth 528, 1.4e-6 further on), so a loop is cut into pieces of
+// 128 whose sums the epilogue adds up in registers, to the nearest.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "hnd_bounds.cuh"
+
+namespace hnd {
+namespace ffn {
+
+constexpr int kThreads = 320;          // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kBK = 64;                // depth of a stage
+constexpr int kHalf = 128 * kBK * 2;   // bytes of A (and of B) per CTA and stage
+constexpr int kStage = 2 * kHalf;
+constexpr int kStoreBytes = 32 * 128 * 2;   // one TMA store: 32 rows n of 128 m
+
+// One stretch of a K loop.
+struct Seg {
+  int a, b0, b1;             // tensor maps; b1 is the second CTA's B
+  int a_mn, b_mn;            // 1: the tile's m (n) axis is contiguous in memory
+  int a_batched, b_batched;  // the map's third coordinate follows the batch
+  int ncols;                 // columns over the pair: 256, 128 or 64
+  int acc;                   // first accumulator column
+  int clear;                 // starts this accumulator
+  int kblocks;               // stages per batch of the K loop
+};
+
+enum OutKind {
+  kOutTma = 0,      // bf16 by TMA
+  kOutBf16 = 1,     // bf16, a lane's elements one by one
+  kOutF32 = 2,      // the same in fp32
+  kOutTok = 3       // token-major: a lane's columns are adjacent
+};
+
+// One product: tiles [batches][mt][nt][splits].
+struct Job {
+  int seg0, nseg;
+  int batches, mt, nt, splits;
+  int kbatches;              // batches of the K loop (weight gradients)
+  long long M, N;            // extents of D
+  int kind, map;             // how D leaves, and the map of kOutTma
+  void* ptr;                 // D otherwise: element (m, n) of split s at
+  long long bs, rs;          //   s bs + n rs + m, or with group > 0 at
+  long long group, gs;       //   (m / group) gs + n rs + m % group; kOutTok: m rs + n
+};
+
+constexpr int kMaxMaps = 10, kMaxSegs = 4, kMaxJobs = 3;
+
+struct Params {
+  CUtensorMap map[kMaxMaps];
+  Seg seg[kMaxSegs];
+  Job job[kMaxJobs];
+  int jobs, tiles;
+  int planes;                // 1, or 3 for fp32
+  int a_plane, b_plane;      // third-coordinate distance of the planes
+  int act;
+  // fp32: the hidden planes [3][n][pitch]
+  __nv_bfloat16* hid[3];
+  long long hid_plane, hid_rs;
+  int hmap[3];               // bf16: their maps
+  int* status;
+};
+
+enum Epi { kEpiOut = 0, kEpiHidden = 1, kEpiGrad = 2 };
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t s32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared location in the pair's leading CTA.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase; after two seconds records a timeout and gives up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int* status) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    for (int i = 0; i < 32; ++i)
+      if (bar_try(bar, parity)) return true;
+    if (now_ns() - t0 > 2000000000ull) break;
+  }
+  if (status) atomicCAS(status, 0, 6 /* HYENA_ND_ERR_DEVICE_TIMEOUT */);
+  return false;
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(src),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[N], uint32_t addr);
+template <>
+__device__ __forceinline__ void tmem_load<32>(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_load<16>(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_all(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major: rows of 64 k,
+// eight rows 1024 bytes apart.  MN-major: rows of 64 m (n), one row a k; eight
+// rows 1024 bytes apart (stride offset), the next 64 m 8192 bytes on (leading
+// offset).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, int mn) {
+  const uint64_t lead = mn ? 8192 >> 4 : 1, stride = 1024 >> 4;
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | lead << 16 | stride << 32 | 1ull << 46 | 2ull << 61;
+}
+// bf16 x bf16 -> fp32, 256 x ncols over the pair.
+__device__ __forceinline__ uint32_t instruction(int a_mn, int b_mn, int ncols) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(a_mn) << 15 | static_cast<uint32_t>(b_mn) << 16 |
+         static_cast<uint32_t>(ncols >> 3) << 17 | static_cast<uint32_t>(256 >> 4) << 24;
+}
+
+// --------------------------------------------------------------- activation
+template <bool F32>
+__device__ __forceinline__ float exp_of(float x) {
+  return F32 ? expf(x) : __expf(x);
+}
+template <bool F32>
+__device__ __forceinline__ float over(float a, float b) {
+  return F32 ? a / b : __fdividef(a, b);
+}
+constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+
+// act(g)
+template <bool F32>
+__device__ __forceinline__ float act_of(int act, float g) {
+  if (act) return g * (0.5f + 0.5f * erff(g * kSqrtHalf));
+  // the fast quotient wants a denominator below 2^126; beyond e^87 the result is below 1e-35 anyway
+  return over<F32>(g, 1.f + exp_of<F32>(fminf(-g, 87.f)));
+}
+// act(g) and act'(g)
+template <bool F32>
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
+  if (act) {
+    const float cdf = 0.5f + 0.5f * erff(g * kSqrtHalf);
+    a = g * cdf;
+    da = cdf + g * kInvSqrt2Pi * exp_of<F32>(-0.5f * g * g);
+  } else {
+    const float s = over<F32>(1.f, 1.f + exp_of<F32>(fminf(-g, 87.f)));
+    a = g * s;
+    da = s * (1.f + g * (1.f - s));
+  }
+}
+
+// H, dG and dU of one position and hidden channel.
+template <bool F32>
+__device__ __forceinline__ void hidden_grads(int act, float g, float u, float d, float (&r)[3]) {
+  float a, da;
+  act_both<F32>(act, g, a, da);
+  r[0] = a * u;
+  r[1] = d * u * da;
+  r[2] = d * a;
+}
+
+__device__ __forceinline__ void stage_put(uint32_t addr, float v) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&h)));
+}
+
+// The bf16 planes of an fp32 value.  Values beyond bf16's largest keep a
+// finite high plane.
+__device__ __forceinline__ void split3(float v, __nv_bfloat16& hi, __nv_bfloat16& mid, __nv_bfloat16& lo) {
+  hi = __float2bfloat16_rn(v);
+  if (fabsf(__bfloat162float(hi)) > 3.4e38f && fabsf(v) <= 3.4028235e38f) hi = __float2bfloat16_rz(v);
+  const float r = v - __bfloat162float(hi);
+  mid = __float2bfloat16_rn(r);
+  lo = __float2bfloat16_rn(r - __bfloat162float(mid));
+}
+
+// ------------------------------------------------------------------- kernel
+struct Tile {
+  int job, split, batch, mt, nt;
+};
+
+// Tiles run in groups of eight m tiles over all n tiles, so that the tiles in
+// flight share both operands in L2.
+__device__ __forceinline__ Tile tile_of(const Params& p, int t) {
+  Tile r{};
+  for (; r.job < p.jobs - 1; ++r.job) {
+    const Job& j = p.job[r.job];
+    const int n = j.batches * j.mt * j.nt * j.splits;
+    if (t < n) break;
+    t -= n;
+  }
+  const Job& j = p.job[r.job];
+  const int mm = j.batches * j.mt, per = mm * j.nt;
+  r.split = t / per;
+  t -= r.split * per;
+  const int g = t / (8 * j.nt), rows = min(8, mm - 8 * g);
+  t -= g * 8 * j.nt;
+  r.nt = t / rows;
+  const int m = 8 * g + t % rows;
+  r.batch = m / j.mt;
+  r.mt = m % j.mt;
+  return r;
+}
+
+// The stages [lo, hi) of a segment that a split takes.
+__device__ __forceinline__ void k_range(const Job& j, const Seg& s, int split, int& lo, int& hi) {
+  const int all = j.kbatches * s.kblocks, per = (all + j.splits - 1) / j.splits;
+  lo = min(all, split * per);
+  hi = min(all, lo + per);
+}
+
+// fp32: the pieces a tile's K loop is added up in, and one of them.
+template <int PIECE>
+__device__ __forceinline__ int pieces_of(const Params& p, const Job& j, int split) {
+  int lo, hi;
+  k_range(j, p.seg[j.seg0], split, lo, hi);
+  return PIECE < 1 << 30 ? (hi - lo + PIECE - 1) / PIECE : 1;
+}
+template <int PIECE>
+__device__ __forceinline__ void k_piece(const Job& j, const Seg& s, int split, int piece, int& lo, int& hi) {
+  k_range(j, s, split, lo, hi);
+  if (PIECE < 1 << 30) {
+    lo += piece * PIECE;
+    hi = min(hi, lo + PIECE);
+  }
+}
+
+// Plane products of fp32 operands, the smallest first.
+__device__ __forceinline__ void planes_of(int combo, int& a, int& b) {
+  a = (0x201100 >> (4 * (5 - combo))) & 0xF;   // low high, high low, mid mid, mid high, high mid, high high
+  b = (0x021010 >> (4 * (5 - combo))) & 0xF;
+}
+
+template <int EPI, bool F32>
+struct Plan {
+  static constexpr int kBufs = EPI == kEpiGrad && !F32 ? 1 : 2;     // accumulators of 256 columns (or one of 384)
+  // columns of a tile: hidden channels, or columns of D.  fp32 halves them: a
+  // thread holds its columns' sums in registers, 64 to 96 of the 168 it has
+  static constexpr int kCols = (EPI == kEpiOut ? 256 : 128) / (F32 ? 2 : 1);
+  static constexpr int kPiece = F32 ? 2 : 1 << 30;                  // stages added up in tensor memory
+  static constexpr int kStages = EPI == kEpiGrad ? 5 : 6;
+  static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;             // tensors stored together
+  static constexpr int kStoreBufs = EPI == kEpiGrad ? 1 : 2;        // per half of the epilogue
+  static constexpr int kSmem =
+      1024 + kStages * kStage + 2 * kOuts * kStoreBufs * kStoreBytes + 8 * (2 * kStages + 2 * kBufs) + 16;
+};
+
+template <int EPI, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_gemm(const __grid_constant__ Params p) {
+  using PL = Plan<EPI, F32>;
+  extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
+  const uint32_t base = (s32(hnd_dyn_smem) + 1023) & ~1023u;
+  const uint32_t out = base + PL::kStages * kStage;
+  const uint32_t bars = out + 2 * PL::kOuts * PL::kStoreBufs * kStoreBytes;
+  const uint32_t full = bars, empty = full + 8 * PL::kStages, accf = empty + 8 * PL::kStages,
+                 acce = accf + 8 * PL::kBufs, tmem_slot = acce + 8 * PL::kBufs;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int combos = F32 ? 6 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < PL::kStages; ++i) bar_init(full + 8 * i, 1), bar_init(empty + 8 * i, 1);
+    for (int i = 0; i < PL::kBufs; ++i) bar_init(accf + 8 * i, 1), bar_init(acce + 8 * i, 16);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tmem_slot) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tmem_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+
+  bool ok = true;
+  if (warp == 0) {
+    // ---- TMA: this CTA's 128 rows of A and its half of B
+    if (lane == 0) {
+      int st = 0, ph = 0;
+      for (int t = pair; ok && t < p.tiles; t += pairs) {
+        const Tile ti = tile_of(p, t);
+        const Job& j = p.job[ti.job];
+        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
+        for (int pc = 0; ok && pc < pieces * combos; ++pc) {
+          int pa = 0, pb = 0;
+          if (F32) planes_of(pc % combos, pa, pb);
+          for (int si = 0; ok && si < j.nseg; ++si) {
+            const Seg& s = p.seg[j.seg0 + si];
+            int lo, hi;
+            k_piece<PL::kPiece>(j, s, ti.split, pc / combos, lo, hi);
+            const CUtensorMap* ma = &p.map[s.a];
+            const CUtensorMap* mb = &p.map[rank ? s.b1 : s.b0];
+            const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
+            const bool dual = s.b0 != s.b1;
+            const int half_n = s.ncols / 2;
+            const int n0 = dual ? ti.nt * half_n : ti.nt * s.ncols + static_cast<int>(rank) * half_n;
+            // MN-major boxes are 64 wide, also where 32 of them are used
+            const uint32_t bytes = 2 * (kHalf + 2 * kBK * (s.b_mn && half_n < 64 ? 64 : half_n));
+            for (int kb = lo; kb < hi; ++kb) {
+              if (!bar_wait(empty + 8 * st, ph ^ 1, p.status)) {
+                ok = false;
+                break;
+              }
+              const int kbat = j.kbatches > 1 ? kb / s.kblocks : 0, k = (kb - kbat * s.kblocks) * kBK;
+              const int bat = j.kbatches > 1 ? kbat : ti.batch;
+              const int za = pa * p.a_plane + (s.a_batched ? bat : 0), zb = pb * p.b_plane + (s.b_batched ? bat : 0);
+              const uint32_t sa = base + st * kStage, sb = sa + kHalf, bar = in_leader(full + 8 * st);
+              if (rank == 0) bar_expect(full + 8 * st, bytes);
+              if (s.a_mn) {
+                tma_load(sa, ma, bar, m0, k, za);
+                tma_load(sa + 8192, ma, bar, m0 + 64, k, za);
+              } else {
+                tma_load(sa, ma, bar, k, m0, za);
+              }
+              if (s.b_mn) {
+                tma_load(sb, mb, bar, n0, k, zb);
+                if (half_n > 64) tma_load(sb + 8192, mb, bar, n0 + 64, k, zb);
+              } else {
+                tma_load(sb, mb, bar, k, n0, zb);
+              }
+              if (++st == PL::kStages) st = 0, ph ^= 1;
+            }
+          }
+        }
+      }
+      if (!ok) {   // copies in flight land before the shared memory goes: they take microseconds
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 20000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA: one thread of the leading CTA
+    if (rank == 0 && lane == 0) {
+      int st = 0, ph = 0, buf = 0, bph = 0;
+      for (int t = pair; ok && t < p.tiles; t += pairs) {
+        const Tile ti = tile_of(p, t);
+        const Job& j = p.job[ti.job];
+        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
+        for (int pc = 0; ok && pc < pieces; ++pc) {
+        if (!bar_wait(acce + 8 * buf, bph ^ 1, p.status)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        for (int c = 0; ok && c < combos; ++c)
+          for (int si = 0; ok && si < j.nseg; ++si) {
+            const Seg& s = p.seg[j.seg0 + si];
+            int lo, hi;
+            k_piece<PL::kPiece>(j, s, ti.split, pc, lo, hi);
+            const uint32_t id = instruction(s.a_mn, s.b_mn, s.ncols), d = tmem + buf * 256 + s.acc;
+            const uint32_t da = s.a_mn ? 2048 >> 4 : 32 >> 4, db = s.b_mn ? 2048 >> 4 : 32 >> 4;
+            bool add = c > 0 || !s.clear;
+            for (int kb = lo; kb < hi; ++kb) {
+              if (!bar_wait(full + 8 * st, ph, p.status)) {
+                ok = false;
+                break;
+              }
+              tmem_fence_after();
+              const uint32_t sa = base + st * kStage;
+              const uint64_t a = operand(sa, s.a_mn), b = operand(sa + kHalf, s.b_mn);
+#pragma unroll
+              for (int i = 0; i < kBK / 16; ++i) {
+                mma(d, a + i * da, b + i * db, id, add);
+                add = true;
+              }
+              mma_commit(empty + 8 * st);
+              if (++st == PL::kStages) st = 0, ph ^= 1;
+            }
+          }
+        mma_commit(accf + 8 * buf);
+        if (++buf == PL::kBufs) buf = 0, bph ^= 1;
+        }
+      }
+    }
+  } else {
+    // ---- epilogue: two halves of four warps, each half takes half the columns
+    const int quad = warp % 4, half = (warp - 2) / 4, row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const bool issuer = (warp == 2 || warp == 6) && lane == 0;
+    const uint32_t stage = out + half * (PL::kOuts * PL::kStoreBufs * kStoreBytes);
+    int buf = 0, bph = 0, sbuf = 0;
+    // all four warps of the half go on, or none: they meet at barriers below
+    auto arrived = [&] {
+      const bool yes = named_all(1 + half, 128, bar_wait(accf + 8 * buf, bph, p.status));
+      tmem_fence_after();
+      return yes;
+    };
+    auto release = [&] {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(in_leader(acce + 8 * buf));
+      if (++buf == PL::kBufs) buf = 0, bph ^= 1;
+    };
+    for (int t = pair; t < p.tiles; t += pairs) {
+      const Tile ti = tile_of(p, t);
+      const Job& j = p.job[ti.job];
+      const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
+      const long long m = m0 + row;
+      const bool live = m < j.M;
+      if constexpr (F32) {
+        // sum[q][i]: product q of the tile at this half's column i
+        constexpr int Q = EPI == kEpiOut ? 1 : EPI == kEpiHidden ? 2 : 3;
+        constexpr int W = PL::kCols / 2;
+        float sum[Q][W];
+        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
+        bool yes = true;
+        for (int pc = 0; pc < pieces; ++pc) {
+          if (!(yes = arrived())) break;
+          const uint32_t acc = tmem + lanes + buf * 256 + half * W;
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int c0 = 0; c0 < W; c0 += 32) {
+              uint32_t v[32];
+              tmem_load(v, acc + q * PL::kCols + c0);
+              tmem_wait_load();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sum[q][c0 + i] = pc ? sum[q][c0 + i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+            }
+          release();
+        }
+        if (!yes) break;
+        const int n0 = ti.nt * PL::kCols + half * W;
+        if constexpr (EPI == kEpiOut) {
+          if (j.kind == kOutF32) {
+            const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
+            float* o = static_cast<float*>(j.ptr) + (j.splits > 1 ? ti.split * j.bs : 0) + at;
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = sum[0][i];
+          } else {
+            // token-major: a lane's columns are adjacent (N is a multiple of 8)
+            float* o = static_cast<float*>(j.ptr) + m * j.rs + n0;
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+              if (live && n0 + i < j.N)
+                *HND_G(reinterpret_cast<float4*>(o + i)) =
+                    make_float4(sum[0][i], sum[0][i + 1], sum[0][i + 2], sum[0][i + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            float r[PL::kOuts];
+            if constexpr (EPI == kEpiGrad) {
+              hidden_grads<true>(p.act, sum[0][i], sum[1][i], sum[2][i], r);
+            } else {
+              r[0] = act_of<true>(p.act, sum[0][i]) * sum[1][i];
+            }
+            if (live && n0 + i < j.N)
+#pragma unroll
+              for (int q = 0; q < PL::kOuts; ++q) {
+                __nv_bfloat16 h[3];
+                split3(r[q], h[0], h[1], h[2]);
+                __nv_bfloat16* o = p.hid[q] + (n0 + i) * p.hid_rs + m;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *HND_G(o + k * p.hid_plane) = h[k];
+              }
+          }
+        }
+      } else {
+        if (!arrived()) break;
+        const uint32_t acc = tmem + lanes + buf * 256;
+        if constexpr (EPI == kEpiOut) {
+          const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            const int n0 = ti.nt * 256 + half * 128 + c0;
+            uint32_t v[32];
+            tmem_load(v, acc + half * 128 + c0);
+            tmem_wait_load();
+            if (c0 == 96) release();
+            if (j.kind == kOutTma) {
+              const uint32_t sb = stage + sbuf * kStoreBytes;
+              if (issuer) store_wait_read<PL::kStoreBufs - 1>();
+              named_sync(1 + half, 128);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) stage_put(sb + i * 256 + row * 2, __uint_as_float(v[i]));
+              fence_async();
+              named_sync(1 + half, 128);
+              if (issuer && m0 < j.M && n0 < j.N) tma_store(&p.map[j.map], sb, m0, n0, ti.batch);
+              if (issuer) store_commit();
+              sbuf = (sbuf + 1) % PL::kStoreBufs;
+            } else if (j.kind == kOutBf16) {
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(j.ptr) + at;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __float2bfloat16_rn(__uint_as_float(v[i]));
+            } else if (j.kind == kOutF32) {
+              float* o = static_cast<float*>(j.ptr) + ti.split * j.bs + m;      // a split's part of a weight gradient
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __uint_as_float(v[i]);
+            } else {
+              // token-major: a lane's columns are adjacent (N is a multiple of 8)
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(j.ptr) + m * j.rs + n0;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                if (live && n0 + i < j.N) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * q]),
+                                                                   __uint_as_float(v[i + 2 * q + 1]));
+                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
+                  }
+                  *HND_G(reinterpret_cast<uint4*>(o + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+          }
+        } else {
+          // hidden channels n of this half: [64 half, 64 half + 64) of the tile's 128
+          constexpr int W = EPI == kEpiGrad ? 16 : 32;
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            const int nc = half * 64 + c0, n0 = ti.nt * 128 + nc;
+            const uint32_t sb = stage + sbuf * kStoreBytes;
+            if (issuer) store_wait_read<PL::kStoreBufs - 1>();
+            named_sync(1 + half, 128);
+#pragma unroll
+            for (int w0 = 0; w0 < 32; w0 += W) {
+              uint32_t g[W], u[W], d[EPI == kEpiGrad ? W : 1];
+              tmem_load(g, acc + nc + w0);
+              tmem_load(u, acc + 128 + nc + w0);
+              if constexpr (EPI == kEpiGrad) tmem_load(d, acc + 256 + nc + w0);
+              tmem_wait_load();
+              if (c0 + w0 == 64 - W) release();
+#pragma unroll
+              for (int i = 0; i < W; ++i) {
+                const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
+                float r[PL::kOuts];
+                if constexpr (EPI == kEpiGrad)
+                  hidden_grads<false>(p.act, gv, uv, __uint_as_float(d[i]), r);
+                else
+                  r[0] = act_of<false>(p.act, gv) * uv;
+#pragma unroll
+                for (int q = 0; q < PL::kOuts; ++q)
+                  stage_put(sb + q * (PL::kStoreBufs * kStoreBytes) + (w0 + i) * 256 + row * 2, r[q]);
+              }
+            }
+            fence_async();
+            named_sync(1 + half, 128);
+            if (issuer) {
+              if (m0 < j.M && n0 < j.N)
+#pragma unroll
+                for (int q = 0; q < PL::kOuts; ++q)
+                  tma_store(&p.map[p.hmap[q]], sb + q * (PL::kStoreBufs * kStoreBytes), m0, n0, ti.batch);
+              store_commit();
+            }
+            sbuf = (sbuf + 1) % PL::kStoreBufs;
+          }
+        }
+      }
+    }
+    if (issuer) store_wait_read<0>();
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+}  // namespace ffn
+}  // namespace hnd

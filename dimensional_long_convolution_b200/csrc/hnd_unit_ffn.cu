@@ -1,174 +1,407 @@
-// The gated feed-forward block over the channels of each position.
+// The gated feed-forward block over the channels of each position: operand
+// layouts, the sequence of products, and the small kernels around them.
 #include "hnd_block.h"
+#include "hnd_ffn_gemm.cuh"
+#include "hnd_host_util.h"
 #include "hnd_io.cuh"
+#include "hnd_launch.h"
 
 namespace hnd {
 
-// A matrix whose column j lies at (j / L) bs + j % L and whose row i adds i rs:
-// activations [B, C, L] are such a matrix [C, B L], weights one with L = cols.
+using bf16 = __nv_bfloat16;
+using namespace ffn;
+
+// ------------------------------------------------------------ small kernels
+
+// [B, C, L] -> rows c of B L adjacent positions at `pitch`: bf16 as it is,
+// fp32 as three bf16 planes.  Used where samples are too short or too ragged
+// for TMA, and for every fp32 operand (weights and token-major activations
+// are B = 1).
 template <class TT>
-struct View {
-  TT* p;
-  long long L, bs, rs;
-  __device__ TT* at(long long i, long long j) const { return p + (j / L) * bs + i * rs + j % L; }
+__global__ void __launch_bounds__(256)
+    k_ffn_pack(const TT* __restrict__ x, bf16* __restrict__ out, long long C, long long L, long long T, long long pitch,
+               long long plane) {
+  const long long groups = pitch / 8, n = groups * C;
+  for (long long g = blockIdx.x * 256LL + threadIdx.x; g < n; g += gridDim.x * 256LL) {
+    const long long c = g / groups, t0 = g % groups * 8;
+    long long b = t0 / L, l = t0 % L;
+    __align__(16) bf16 v[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f = 0.f;
+      if (t0 + i < T) f = ld1(x + (b * C + c) * L + l);
+      if (++l == L) l = 0, ++b;
+      if (sizeof(TT) == 4)
+        split3(f, v[0][i], v[1][i], v[2][i]);
+      else
+        v[0][i] = __float2bfloat16_rn(f);
+    }
+#pragma unroll
+    for (int k = 0; k < (sizeof(TT) == 4 ? 3 : 1); ++k)
+      *HND_G(reinterpret_cast<uint4*>(out + k * plane + c * pitch + t0)) = *reinterpret_cast<const uint4*>(v[k]);
+  }
+}
+
+// The sum of a weight gradient's partial products, in the order of the splits.
+template <class TT>
+__global__ void __launch_bounds__(256)
+    k_ffn_sum(const float* __restrict__ part, TT* __restrict__ out, long long n, int splits) {
+  for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 4; i < n; i += gridDim.x * 1024LL) {
+    float4 s = *HND_G(reinterpret_cast<const float4*>(part + i));
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = *HND_G(reinterpret_cast<const float4*>(part + k * n + i));
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    st1(out + i, s.x), st1(out + i + 1, s.y), st1(out + i + 2, s.z), st1(out + i + 3, s.w);
+  }
+}
+
+// ----------------------------------------------------------------- planning
+static long long up(long long v, long long a) { return (v + a - 1) / a * a; }
+static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+constexpr int kPairs = 74;   // CTA pairs of a B200
+
+// Where everything lies in the workspace, a function of the descriptor alone.
+struct Layout {
+  bool token, packed;        // token-major operands; samples gathered into rows of all positions
+  int planes;
+  long long batches, Lx;     // of the position axis as the products see it
+  long long pitch;           // of packed rows (token: of a position's channels)
+  long long hpitch;          // of the hidden rows
+  size_t x, dy, w, hid, part, bytes;
+  long long act_plane, w_plane, hid_plane;   // elements
+  int splits;
 };
 
-__device__ __forceinline__ float act_value(int act, float g) {
-  return act ? g * 0.5f * (1.f + erff(g * 0.70710678118654752f)) : g / (1.f + expf(-g));
-}
-__device__ __forceinline__ float act_slope(int act, float g) {
-  if (act) return 0.5f * (1.f + erff(g * 0.70710678118654752f)) + g * 0.39894228040143268f * expf(-0.5f * g * g);
-  const float s = 1.f / (1.f + expf(-g));
-  return s * (1.f + g * (1.f - s));
-}
-
-constexpr int kGT = 64, kGK = 16;
-
-// acc += A B over k, A(m, k) = a(m, k) or a(k, m) (TA), B(k, n) = b(k, n) or b(n, k) (TB).
-template <bool TA, bool TB, class TT>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], const View<const TT>& a, const View<const TT>& b,
-                                             long long M, long long N, long long K, long long m0, long long n0,
-                                             float (*sa)[kGT + 1], float (*sb)[kGT + 1]) {
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  float part[4][4] = {};      // sums of 256 terms at a time keep the rounding of long sums small
-  for (long long k0 = 0; k0 < K; k0 += kGK) {
-    __syncthreads();
-    for (int i = tid; i < kGT * kGK; i += 256) {
-      const int k = TA ? i / kGT : i % kGK, m = TA ? i % kGT : i / kGK;
-      sa[k][m] = (m0 + m < M && k0 + k < K) ? ld1(TA ? a.at(k0 + k, m0 + m) : a.at(m0 + m, k0 + k)) : 0.f;
-    }
-    for (int i = tid; i < kGT * kGK; i += 256) {
-      const int k = TB ? i % kGK : i / kGT, n = TB ? i / kGK : i % kGT;
-      sb[k][n] = (n0 + n < N && k0 + k < K) ? ld1(TB ? b.at(n0 + n, k0 + k) : b.at(k0 + k, n0 + n)) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kGK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) part[i][q] += sa[k][ty * 4 + i] * sb[k][tx * 4 + q];
-    if (k0 % 256 == 256 - kGK || k0 + kGK >= K)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][q] += part[i][q], part[i][q] = 0.f;
+// Fewest splits of the weight gradients' K loops that fill the pairs: rounds
+// of tiles times the stages of each, with 8 stages' worth for a tile's ends.
+static int weight_splits(long long C, long long F, long long stages, int cols) {
+  const long long tiles = 2 * cdiv(C, 256) * cdiv(F, cols) + cdiv(F, 256) * cdiv(C, cols);
+  int best = 1;
+  long long cost = 0;
+  for (int s = 1; s <= 32 && (s == 1 || stages / s >= 4); ++s) {
+    const long long c = cdiv(tiles * s, kPairs) * (cdiv(stages, s) + 8) + (s > 1 ? 4 : 0);
+    if (s == 1 || c < cost) best = s, cost = c;
   }
+  return best;
 }
 
-#define FFN_TILE                                                              \
-  __shared__ float sa[kGK][kGT + 1], sb[kGK][kGT + 1];                        \
-  const long long m0 = blockIdx.y * static_cast<long long>(kGT), n0 = blockIdx.x * static_cast<long long>(kGT); \
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+static Layout layout(const FfnArgs& a, bool backward) {
+  Layout l{};
+  const long long T = a.B * a.L;
+  l.planes = a.bf16 ? 1 : 3;
+  l.token = a.L == 1;
+  // A row of positions has to start on 16 bytes for TMA, and a sample's last
+  // tile of 256 positions should not be mostly empty: gathering costs one
+  // pass over the activations, an empty half tile half the products.
+  l.packed = !l.token && (!a.bf16 || a.L % 8 || (a.B > 1 && 4 * up(a.L, 256) > 5 * a.L));
+  const bool merged = l.token || l.packed;
+  l.batches = merged ? 1 : a.B;
+  l.Lx = merged ? T : a.L;
+  l.pitch = l.token ? a.C : up(T, 8);
+  l.hpitch = up(l.Lx, 8);
+  const bool copied = l.packed || !a.bf16;
+  size_t at = 0;
+  auto take = [&](long long elements, size_t size) {
+    const size_t here = at;
+    at += (static_cast<size_t>(elements) * size + 255) / 256 * 256;
+    return here;
+  };
+  l.act_plane = l.token ? T * a.C : a.C * l.pitch;
+  l.w_plane = a.C * a.F;
+  l.hid_plane = l.batches * a.F * l.hpitch;
+  if (copied) l.x = take(l.planes * l.act_plane, 2);
+  if (copied && backward) l.dy = take(l.planes * l.act_plane, 2);
+  if (!a.bf16) l.w = take(9 * l.w_plane, 2);
+  l.hid = take((backward ? 3 : 1) * l.planes * l.hid_plane, 2);
+  l.splits = 1;
+  if (backward) {
+    // every split gets a stage at least
+    const long long stages = l.batches * cdiv(l.Lx, kBK);
+    const long long per = cdiv(stages, weight_splits(a.C, a.F, stages * (a.bf16 ? 1 : 6), a.bf16 ? 256 : 128));
+    l.splits = static_cast<int>(cdiv(stages, per));
+    if (l.splits > 1) l.part = take(3 * l.splits * l.w_plane, 4);
+  }
+  l.bytes = at;
+  return l;
+}
 
-// H = act(Wg X) (Wu X)
-template <class TT>
-__global__ void __launch_bounds__(256) k_ffn_hidden(View<const TT> x, View<const TT> wg, View<const TT> wu,
-                                                    View<TT> h, long long C, long long F, long long T, int act) {
-  FFN_TILE
-  float g[4][4] = {}, u[4][4] = {};
-  tile_product<false, false>(g, wg, x, F, T, C, m0, n0, sa, sb);
-  tile_product<false, false>(u, wu, x, F, T, C, m0, n0, sa, sb);
-  for (int i = 0; i < 4; ++i)
-    for (int q = 0; q < 4; ++q) {
-      const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + q;
-      if (m < F && n < T) st1(h.at(m, n), act_value(act, g[i][q]) * u[i][q]);
+size_t ffn_workspace(const FfnArgs& a, bool backward) { return layout(a, backward).bytes; }
+
+// ---------------------------------------------------------------- tensor maps
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A bf16 matrix in memory: `rows` rows of `inner` adjacent elements, `count` of them `batch` elements apart.
+struct Mat {
+  const void* p;
+  long long inner, rows, count, pitch, batch;
+};
+
+static bool encode(CUtensorMap* map, const Mat& m, int box_inner, int box_rows, bool swizzled) {
+  const EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dim[3] = {static_cast<cuuint64_t>(m.inner), static_cast<cuuint64_t>(m.rows),
+                             static_cast<cuuint64_t>(m.count)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(m.pitch) * 2, static_cast<cuuint64_t>(m.batch) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(m.p), dim, stride, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// -------------------------------------------------------------------- launch
+struct Launch {
+  Params p{};
+  int maps = 0, segs = 0;
+  bool ok = true;
+
+  int add(const Mat& m, int box_inner, int box_rows, bool swizzled) {
+    if (maps == kMaxMaps || !encode(&p.map[maps], m, box_inner, box_rows, swizzled)) {
+      ok = false;
+      return 0;
     }
+    return maps++;
+  }
+  // an operand whose tile axis (m or n) is contiguous / whose k axis is
+  int mn(const Mat& m) { return add(m, 64, kBK, true); }
+  int km(const Mat& m, int rows = 128) { return add(m, kBK, rows, true); }
+  int store(const Mat& m) { return add(m, 128, 32, false); }
+  void job(const Job& j) { p.job[p.jobs++] = j; }
+};
+
+template <int EPI, bool F32>
+static cudaError_t run(Launch& l, cudaStream_t st) {
+  if (!l.ok) return cudaErrorInvalidValue;
+  long long tiles = 0;
+  for (int i = 0; i < l.p.jobs; ++i) {
+    const Job& j = l.p.job[i];
+    tiles += static_cast<long long>(j.batches) * j.mt * j.nt * j.splits;
+  }
+  if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
+  l.p.tiles = static_cast<int>(tiles);
+  auto kern = k_ffn_gemm<EPI, F32>;
+  constexpr int smem = Plan<EPI, F32>::kSmem;
+  static_assert(smem <= static_cast<int>(kMaxSmem), "shared memory");
+  const cudaError_t e = ensure_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  long long pairs = sm_count() / 2;
+  if (pairs > tiles) pairs = tiles;
+  kern<<<static_cast<unsigned>(2 * pairs), kThreads, smem, st>>>(l.p);
+  return cudaGetLastError();
 }
 
-// H, dG, dU from X and dY
-template <class TT>
-__global__ void __launch_bounds__(256)
-    k_ffn_hidden_grad(View<const TT> x, View<const TT> dy, View<const TT> wg, View<const TT> wu, View<const TT> wd,
-                      View<TT> h, View<TT> dg, View<TT> du, long long C, long long F, long long T, int act) {
-  FFN_TILE
-  float g[4][4] = {}, u[4][4] = {}, d[4][4] = {};
-  tile_product<false, false>(g, wg, x, F, T, C, m0, n0, sa, sb);
-  tile_product<false, false>(u, wu, x, F, T, C, m0, n0, sa, sb);
-  tile_product<true, false>(d, wd, dy, F, T, C, m0, n0, sa, sb);
-  for (int i = 0; i < 4; ++i)
-    for (int q = 0; q < 4; ++q) {
-      const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + q;
-      if (m >= F || n >= T) continue;
-      const float a = act_value(act, g[i][q]);
-      st1(h.at(m, n), a * u[i][q]);
-      st1(dg.at(m, n), d[i][q] * u[i][q] * act_slope(act, g[i][q]));
-      st1(du.at(m, n), d[i][q] * a);
-    }
-}
-
-// D = A1 B1 (+ A2 B2)
-template <bool TA, bool TB, class TT>
-__global__ void __launch_bounds__(256)
-    k_ffn_product(View<const TT> a1, View<const TT> b1, View<const TT> a2, View<const TT> b2, View<TT> d, long long M,
-                  long long N, long long K) {
-  FFN_TILE
-  float acc[4][4] = {};
-  tile_product<TA, TB>(acc, a1, b1, M, N, K, m0, n0, sa, sb);
-  if (a2.p) tile_product<TA, TB>(acc, a2, b2, M, N, K, m0, n0, sa, sb);
-  for (int i = 0; i < 4; ++i)
-    for (int q = 0; q < 4; ++q) {
-      const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + q;
-      if (m < M && n < N) st1(d.at(m, n), acc[i][q]);
-    }
-}
-
-static dim3 tiles(long long M, long long N) {
-  return dim3(static_cast<unsigned>((N + kGT - 1) / kGT), static_cast<unsigned>((M + kGT - 1) / kGT));
-}
-
-template <class TT>
+template <bool F32>
 struct Ffn {
+  using TT = typename std::conditional<F32, float, bf16>::type;
+  // columns of a tile: hidden channels, and columns of the other products
+  static constexpr int hn = Plan<kEpiHidden, F32>::kCols, on = Plan<kEpiOut, F32>::kCols;
   const FfnArgs& a;
-  long long T = a.B * a.L;
-  template <class Q>
-  View<Q> grid(Q* p) const {
-    return {p, a.L, a.C * a.L, a.L};
+  const Layout l;
+  const long long T;
+  Mat x, dy, wg, wu, wd, hid[3];
+
+  char* ws(size_t at) const { return static_cast<char*>(a.ws) + at; }
+  bf16* wsb(size_t at) const { return reinterpret_cast<bf16*>(ws(at)); }
+
+  Ffn(const FfnArgs& args, bool backward) : a(args), l(layout(args, backward)), T(args.B * args.L) {
+    const bool copied = l.packed || F32;
+    x = activation(copied ? ws(l.x) : a.x);
+    dy = activation(copied ? ws(l.dy) : a.dy);
+    const void* w[3] = {a.wg, a.wu, a.wd};
+    if (F32)
+      for (int i = 0; i < 3; ++i) w[i] = wsb(l.w) + 3 * i * l.w_plane;
+    wg = weight(w[0], a.F, a.C), wu = weight(w[1], a.F, a.C), wd = weight(w[2], a.C, a.F);
+    for (int i = 0; i < 3; ++i)
+      hid[i] = Mat{wsb(l.hid) + i * l.planes * l.hid_plane, l.Lx, a.F, l.batches * l.planes, l.hpitch, a.F * l.hpitch};
   }
-  template <class Q>
-  View<Q> flat(Q* p, long long cols) const {
-    return {p, cols, 0, cols};
+  Mat activation(const void* p) const {
+    if (l.token) return Mat{p, a.C, T, l.planes, a.C, l.act_plane};
+    if (l.packed) return Mat{p, T, a.C, l.planes, l.pitch, l.act_plane};
+    return Mat{p, a.L, a.C, a.B, a.L, a.C * a.L};
   }
-  const TT* in(const void* p) const { return static_cast<const TT*>(p); }
-  TT* out(void* p) const { return static_cast<TT*>(p); }
-  TT* hidden(int i) const { return out(a.ws) + static_cast<size_t>(i) * T * a.F; }
+  Mat weight(const void* p, long long rows, long long cols) const { return Mat{p, cols, rows, l.planes, cols, l.w_plane}; }
+
+  cudaError_t pack(const void* src, bf16* dst, long long B, long long rows, long long L, long long pitch,
+                   long long plane) const {
+    const long long blocks = cdiv(pitch / 8 * rows, 256);
+    k_ffn_pack<TT><<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, a.stream>>>(
+        static_cast<const TT*>(src), dst, rows, L, B * L, pitch, plane);
+    return cudaGetLastError();
+  }
+  cudaError_t pack_activation(const void* src, size_t at) const {
+    if (l.token) return F32 ? pack(src, wsb(at), 1, T, a.C, a.C, l.act_plane) : cudaSuccess;
+    return l.packed ? pack(src, wsb(at), a.B, a.C, a.L, l.pitch, l.act_plane) : cudaSuccess;
+  }
+  cudaError_t pack_weights() const {
+    if (!F32) return cudaSuccess;
+    const void* w[3] = {a.wg, a.wu, a.wd};
+    for (int i = 0; i < 3; ++i) {
+      const long long rows = i < 2 ? a.F : a.C, cols = i < 2 ? a.C : a.F;
+      const cudaError_t e = pack(w[i], wsb(l.w) + 3 * i * l.w_plane, 1, rows, cols, cols, l.w_plane);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
+
+  Launch start() const {
+    Launch n;
+    n.p.planes = l.planes;
+    n.p.act = a.act;
+    n.p.status = a.status;
+    // plane distances in the third coordinate: a batched operand has its batches in between
+    n.p.a_plane = n.p.b_plane = 1;
+    return n;
+  }
+  // activations as the rows of a product (m = positions): the position axis
+  // is contiguous, except token-major, where the channels are
+  int positions(Launch& n, const Mat& m) const { return l.token ? n.km(m) : n.mn(m); }
+  Seg data_seg(int ma, int mb0, int mb1, bool a_mn, bool b_mn, int ncols, int acc, int clear, long long depth) const {
+    return Seg{ma, mb0, mb1, a_mn, b_mn, l.batches > 1, 0, ncols, acc, clear, static_cast<int>(cdiv(depth, kBK))};
+  }
+  Job data_job(int nseg, long long N, int per_tile) const {
+    Job j{};
+    j.nseg = nseg;
+    j.batches = static_cast<int>(l.batches);
+    j.mt = static_cast<int>(cdiv(l.Lx, 256));
+    j.nt = static_cast<int>(cdiv(N, per_tile));
+    j.splits = j.kbatches = 1;
+    j.M = l.Lx;
+    j.N = N;
+    return j;
+  }
+  void hidden_out(Launch& n, int count) const {
+    for (int i = 0; i < count; ++i) {
+      n.p.hid[i] = static_cast<bf16*>(const_cast<void*>(hid[i].p));
+      if (!F32) n.p.hmap[i] = n.store(hid[i]);
+    }
+    n.p.hid_plane = l.hid_plane;
+    n.p.hid_rs = l.hpitch;
+  }
+  // y or dx: back to the activations' own layout
+  void activation_out(Launch& n, Job& j, void* p) const {
+    j.ptr = p;
+    if (l.token) {
+      j.kind = kOutTok;
+      j.rs = a.C;
+    } else if (l.packed) {
+      j.kind = F32 ? kOutF32 : kOutBf16;
+      j.rs = a.L;
+      j.group = a.L;
+      j.gs = a.C * a.L;
+    } else {
+      j.kind = kOutTma;
+      j.map = n.store(activation(p));
+    }
+  }
 
   cudaError_t forward() const {
-    k_ffn_hidden<TT><<<tiles(a.F, T), 256, 0, a.stream>>>(grid(in(a.x)), flat(in(a.wg), a.C), flat(in(a.wu), a.C),
-                                                          flat(hidden(0), T), a.C, a.F, T, a.act);
-    k_ffn_product<false, false, TT><<<tiles(a.C, T), 256, 0, a.stream>>>(
-        flat(in(a.wd), a.F), flat(in(hidden(0)), T), View<const TT>{}, View<const TT>{}, grid(out(a.y)), a.C, T, a.F);
-    return cudaGetLastError();
+    cudaError_t e;
+    if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_weights()) != cudaSuccess) return e;
+    Launch h = start();
+    h.p.seg[0] = data_seg(positions(h, x), h.km(wg, hn), h.km(wu, hn), !l.token, false, 2 * hn, 0, 1, a.C);
+    hidden_out(h, 1);
+    h.job(data_job(1, a.F, hn));
+    if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
+    Launch y = start();
+    const int m = y.km(wd, on / 2);
+    y.p.seg[0] = data_seg(y.mn(hid[0]), m, m, true, false, on, 0, 1, a.F);
+    Job j = data_job(1, a.C, on);
+    activation_out(y, j, a.y);
+    y.job(j);
+    return run<kEpiOut, F32>(y, a.stream);
   }
+
   cudaError_t backward() const {
-    const auto x = grid(in(a.x)), dy = grid(in(a.dy));
-    const auto wg = flat(in(a.wg), a.C), wu = flat(in(a.wu), a.C);
-    const auto h = flat(in(hidden(0)), T), dg = flat(in(hidden(1)), T), du = flat(in(hidden(2)), T);
-    const View<const TT> none{};
-    k_ffn_hidden_grad<TT><<<tiles(a.F, T), 256, 0, a.stream>>>(x, dy, wg, wu, flat(in(a.wd), a.F), flat(hidden(0), T),
-                                                               flat(hidden(1), T), flat(hidden(2), T), a.C, a.F, T,
-                                                               a.act);
-    k_ffn_product<true, false, TT><<<tiles(a.C, T), 256, 0, a.stream>>>(wg, dg, wu, du, grid(out(a.dx)), a.C, T, a.F);
-    k_ffn_product<false, true, TT>
-        <<<tiles(a.F, a.C), 256, 0, a.stream>>>(dg, x, none, none, flat(out(a.dwg), a.C), a.F, a.C, T);
-    k_ffn_product<false, true, TT>
-        <<<tiles(a.F, a.C), 256, 0, a.stream>>>(du, x, none, none, flat(out(a.dwu), a.C), a.F, a.C, T);
-    k_ffn_product<false, true, TT>
-        <<<tiles(a.C, a.F), 256, 0, a.stream>>>(dy, h, none, none, flat(out(a.dwd), a.F), a.C, a.F, T);
+    cudaError_t e;
+    if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_activation(a.dy, l.dy)) != cudaSuccess ||
+        (e = pack_weights()) != cudaSuccess)
+      return e;
+    // H, dG, dU
+    Launch h = start();
+        h.p.seg[0] = data_seg(positions(h, x), h.km(wg, hn), h.km(wu, hn), !l.token, false, 2 * hn, 0, 1, a.C);
+    const int md = h.mn(wd);
+    h.p.seg[1] = data_seg(positions(h, dy), md, md, !l.token, true, hn, 2 * hn, 1, a.C);
+    hidden_out(h, 3);
+    h.job(data_job(2, a.F, hn));
+    if ((e = run<kEpiGrad, F32>(h, a.stream)) != cudaSuccess) return e;
+    // dX
+    Launch d = start();
+    const int mg = d.mn(wg), mu = d.mn(wu);
+    d.p.seg[0] = data_seg(d.mn(hid[1]), mg, mg, true, true, on, 0, 1, a.F);
+    d.p.seg[1] = data_seg(d.mn(hid[2]), mu, mu, true, true, on, 0, 0, a.F);
+    Job j = data_job(2, a.C, on);
+    activation_out(d, j, a.dx);
+    d.job(j);
+    if ((e = run<kEpiOut, F32>(d, a.stream)) != cudaSuccess) return e;
+    // dWg[f][c] = dG X', dWu[f][c] = dU X', dWd[c][f] = dY H'
+    Launch w = start();
+    const bool batched = l.batches > 1;
+    const int stages = static_cast<int>(cdiv(l.Lx, kBK));
+    const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, on / 2);
+    const int mh = w.km(hid[0]), mdg = w.km(hid[1], on / 2), mdu = w.km(hid[2], on / 2);
+    w.p.seg[0] = Seg{mx, mdg, mdg, l.token, 0, batched, batched, on, 0, 1, stages};
+    w.p.seg[1] = Seg{mx, mdu, mdu, l.token, 0, batched, batched, on, 0, 1, stages};
+    w.p.seg[2] = Seg{mh, mdy, mdy, 0, l.token, batched, batched, on, 0, 1, stages};
+    void* out[3] = {a.dwg, a.dwu, a.dwd};
+    float* part = reinterpret_cast<float*>(ws(l.part));
+    for (int i = 0; i < 3; ++i) {
+      Job q{};
+      q.seg0 = i;
+      q.nseg = 1;
+      q.M = i < 2 ? a.C : a.F;
+      q.N = i < 2 ? a.F : a.C;
+      q.mt = static_cast<int>(cdiv(q.M, 256));
+      q.nt = static_cast<int>(cdiv(q.N, on));
+      q.batches = 1;
+      q.kbatches = static_cast<int>(l.batches);
+      q.splits = l.splits;
+      q.rs = q.M;
+      q.bs = l.w_plane;
+      if (l.splits > 1) {
+        q.kind = kOutF32;
+        q.ptr = part + static_cast<size_t>(i) * l.splits * l.w_plane;
+      } else if (F32) {
+        q.kind = kOutF32;
+        q.ptr = out[i];
+      } else {
+        q.kind = kOutTma;
+        q.map = w.store(Mat{out[i], q.M, q.N, 1, q.M, l.w_plane});
+      }
+      w.job(q);
+    }
+    if ((e = run<kEpiOut, F32>(w, a.stream)) != cudaSuccess) return e;
+    if (l.splits > 1)
+      for (int i = 0; i < 3; ++i) {
+        const long long blocks = cdiv(l.w_plane, 1024);
+        k_ffn_sum<TT><<<static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, a.stream>>>(
+            part + static_cast<size_t>(i) * l.splits * l.w_plane, static_cast<TT*>(out[i]), l.w_plane, l.splits);
+      }
     return cudaGetLastError();
   }
 };
 
-size_t ffn_workspace(const FfnArgs& a, bool backward) {
-  return static_cast<size_t>(backward ? 3 : 1) * a.B * a.L * a.F * (a.bf16 ? 2 : 4);
-}
-
 cudaError_t launch_ffn_forward(const FfnArgs& a) {
-  return a.bf16 ? Ffn<__nv_bfloat16>{a}.forward() : Ffn<float>{a}.forward();
+  return a.bf16 ? Ffn<false>(a, false).forward() : Ffn<true>(a, false).forward();
 }
 
 cudaError_t launch_ffn_backward(const FfnArgs& a) {
-  return a.bf16 ? Ffn<__nv_bfloat16>{a}.backward() : Ffn<float>{a}.backward();
+  return a.bf16 ? Ffn<false>(a, true).backward() : Ffn<true>(a, true).backward();
 }
 
 }  // namespace hnd

@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hnd_bounds.cuh"
 
 namespace hnd {
@@ -239,16 +241,16 @@ __device__ __forceinline__ float over(float a, float b) {
 constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
 
 // act(g)
-template <bool F32>
-__device__ __forceinline__ float act_of(int act, float g) {
-  if (act) return g * (0.5f + 0.5f * erff(g * kSqrtHalf));
+template <bool F32, int ACT>
+__device__ __forceinline__ float act_of(float g) {
+  if (ACT) return g * (0.5f + 0.5f * erff(g * kSqrtHalf));
   // the fast quotient wants a denominator below 2^126; beyond e^87 the result is below 1e-35 anyway
   return over<F32>(g, 1.f + exp_of<F32>(fminf(-g, 87.f)));
 }
 // act(g) and act'(g)
-template <bool F32>
-__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
-  if (act) {
+template <bool F32, int ACT>
+__device__ __forceinline__ void act_both(float g, float& a, float& da) {
+  if (ACT) {
     const float cdf = 0.5f + 0.5f * erff(g * kSqrtHalf);
     a = g * cdf;
     da = cdf + g * kInvSqrt2Pi * exp_of<F32>(-0.5f * g * g);
@@ -260,13 +262,23 @@ __device__ __forceinline__ void act_both(int act, float g, float& a, float& da) 
 }
 
 // H, dG and dU of one position and hidden channel.
-template <bool F32>
-__device__ __forceinline__ void hidden_grads(int act, float g, float u, float d, float (&r)[3]) {
+template <bool F32, int ACT>
+__device__ __forceinline__ void hidden_grads(float g, float u, float d, float (&r)[3]) {
   float a, da;
-  act_both<F32>(act, g, a, da);
+  act_both<F32, ACT>(g, a, da);
   r[0] = a * u;
   r[1] = d * u * da;
   r[2] = d * a;
+}
+
+// The activation as a constant of the code that runs over many values: a
+// branch at each of them would keep their exponentials from overlapping.
+template <class Fn>
+__device__ __forceinline__ void with_act(int act, Fn fn) {
+  if (act)
+    fn(std::integral_constant<int, 1>{});
+  else
+    fn(std::integral_constant<int, 0>{});
 }
 
 __device__ __forceinline__ void stage_put(uint32_t addr, float v) {
@@ -554,13 +566,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
                     make_float4(sum[0][i], sum[0][i + 1], sum[0][i + 2], sum[0][i + 3]);
           }
         } else {
+          with_act(p.act, [&](auto kind) {
+          constexpr int ACT = decltype(kind)::value;
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             float r[PL::kOuts];
             if constexpr (EPI == kEpiGrad) {
-              hidden_grads<true>(p.act, sum[0][i], sum[1][i], sum[2][i], r);
+              hidden_grads<true, ACT>(sum[0][i], sum[1][i], sum[2][i], r);
             } else {
-              r[0] = act_of<true>(p.act, sum[0][i]) * sum[1][i];
+              r[0] = act_of<true, ACT>(sum[0][i]) * sum[1][i];
             }
             if (live && n0 + i < j.N)
 #pragma unroll
@@ -572,6 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
                 for (int k = 0; k < 3; ++k) *HND_G(o + k * p.hid_plane) = h[k];
               }
           }
+          });
         }
       } else {
         if (!arrived()) break;
@@ -638,18 +653,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
               if constexpr (EPI == kEpiGrad) tmem_load(d, acc + 256 + nc + w0);
               tmem_wait_load();
               if (c0 + w0 == 64 - W) release();
+              with_act(p.act, [&](auto kind) {
+                constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-              for (int i = 0; i < W; ++i) {
-                const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
-                float r[PL::kOuts];
-                if constexpr (EPI == kEpiGrad)
-                  hidden_grads<false>(p.act, gv, uv, __uint_as_float(d[i]), r);
-                else
-                  r[0] = act_of<false>(p.act, gv) * uv;
+                for (int i = 0; i < W; ++i) {
+                  const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
+                  float r[PL::kOuts];
+                  if constexpr (EPI == kEpiGrad)
+                    hidden_grads<false, ACT>(gv, uv, __uint_as_float(d[i]), r);
+                  else
+                    r[0] = act_of<false, ACT>(gv) * uv;
 #pragma unroll
-                for (int q = 0; q < PL::kOuts; ++q)
-                  stage_put(sb + q * (PL::kStoreBufs * kStoreBytes) + (w0 + i) * 256 + row * 2, r[q]);
-              }
+                  for (int q = 0; q < PL::kOuts; ++q)
+                    stage_put(sb + q * (PL::kStoreBufs * kStoreBytes) + (w0 + i) * 256 + row * 2, r[q]);
+                }
+              });
             }
             fence_async();
             named_sync(1 + half, 128);

@@ -74,14 +74,17 @@ struct Layout {
   int splits;
 };
 
-// Fewest splits of the weight gradients' K loops that fill the pairs: rounds
-// of tiles times the stages of each, with 8 stages' worth for a tile's ends.
+// Splits of the weight gradients' K loops.  In stages of a pair (0.27 us at
+// full rate): rounds of tiles, each with 8 stages' worth for a tile's ends;
+// split, the partial sums go through memory once each way and one more
+// kernel runs.  C 256, F 1024, 32768 positions: 6 splits, 12 tiles otherwise
+// on 74 pairs; C 2048, F 5632: none (3 would add 67 us of partial sums).
 static int weight_splits(long long C, long long F, long long stages, int cols) {
   const long long tiles = 2 * cdiv(C, 256) * cdiv(F, cols) + cdiv(F, 256) * cdiv(C, cols);
   int best = 1;
   long long cost = 0;
   for (int s = 1; s <= 32 && (s == 1 || stages / s >= 4); ++s) {
-    const long long c = cdiv(tiles * s, kPairs) * (cdiv(stages, s) + 8) + (s > 1 ? 4 : 0);
+    const long long c = cdiv(tiles * s, kPairs) * (cdiv(stages, s) + 8) + (s > 1 ? 15 + s * C * F * 24 / 1750000 : 0);
     if (s == 1 || c < cost) best = s, cost = c;
   }
   return best;

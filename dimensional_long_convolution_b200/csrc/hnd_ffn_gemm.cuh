@@ -60,11 +60,31 @@ enum OutKind {
   kOutTok = 3       // token-major: a lane's columns are adjacent
 };
 
+// Division by a number fixed at launch: n / d = (n mul) >> 32 for 0 <= n <
+// 2^31, with mul = ceil(2^(32 + s) / d) and a shift (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994).  The single
+// threads that issue copies and products find their tile with it: with plain
+// divisions that took longer than a short tile's products.
+struct Div {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int quot(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+};
+inline Div make_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;                 // 2^(s-1) < d <= 2^s
+  if (s == 0) return Div{1, 0, 0};
+  // mul < 2^32 as d > 2^(s-1); exact for n < 2^31
+  return Div{d, static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+
 // One product: tiles [batches][mt][nt][splits].
 struct Job {
   int seg0, nseg;
   int batches, mt, nt, splits;
   int kbatches;              // batches of the K loop (weight gradients)
+  Div per, group8, mdiv;     // tiles of a split, of eight m tiles; mt
   long long M, N;            // extents of D
   int kind, map;             // how D leaves, and the map of kOutTma
   void* ptr;                 // D otherwise: element (m, n) of split s at
@@ -140,8 +160,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int* sta
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Arrives at a barrier of the pair's other CTA.  Only tensor-memory reads come
+// before it, which tcgen05.wait and fence order; release at cluster scope
+// would wait for this thread's stores to memory too (2000 cycles a tile).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -312,15 +335,15 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int t) {
     t -= n;
   }
   const Job& j = p.job[r.job];
-  const int mm = j.batches * j.mt, per = mm * j.nt;
-  r.split = t / per;
-  t -= r.split * per;
-  const int g = t / (8 * j.nt), rows = min(8, mm - 8 * g);
-  t -= g * 8 * j.nt;
-  r.nt = t / rows;
-  const int m = 8 * g + t % rows;
-  r.batch = m / j.mt;
-  r.mt = m % j.mt;
+  const int mm = j.batches * j.mt;
+  r.split = j.per.quot(t);
+  t -= r.split * static_cast<int>(j.per.d);
+  const int g = j.group8.quot(t), rows = min(8, mm - 8 * g);
+  t -= g * static_cast<int>(j.group8.d);
+  r.nt = rows == 8 ? t >> 3 : t / rows;
+  const int m = 8 * g + t - r.nt * rows;
+  r.batch = j.mdiv.quot(m);
+  r.mt = m - r.batch * j.mt;
   return r;
 }
 
@@ -459,8 +482,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
     // ---- MMA: one thread of the leading CTA
     if (rank == 0 && lane == 0) {
       int st = 0, ph = 0, buf = 0, bph = 0;
+      const bool alike = p.jobs == 1 && p.job[0].splits == 1;      // every tile has the same K loop
       for (int t = pair; ok && t < p.tiles; t += pairs) {
-        const Tile ti = tile_of(p, t);
+        const Tile ti = alike ? Tile{} : tile_of(p, t);
         const Job& j = p.job[ti.job];
         const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
         for (int pc = 0; ok && pc < pieces; ++pc) {

@@ -193,10 +193,14 @@ static cudaError_t run(Launch& l, cudaStream_t st) {
   if (!l.ok) return cudaErrorInvalidValue;
   long long tiles = 0;
   for (int i = 0; i < l.p.jobs; ++i) {
-    const Job& j = l.p.job[i];
-    tiles += static_cast<long long>(j.batches) * j.mt * j.nt * j.splits;
+    Job& j = l.p.job[i];
+    const long long per = static_cast<long long>(j.batches) * j.mt * j.nt;
+    tiles += per * j.splits;
+    if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
+    j.per = make_div(static_cast<uint32_t>(per));
+    j.group8 = make_div(static_cast<uint32_t>(8 * j.nt));
+    j.mdiv = make_div(static_cast<uint32_t>(j.mt));
   }
-  if (tiles >= 1LL << 31) return cudaErrorInvalidValue;
   l.p.tiles = static_cast<int>(tiles);
   auto kern = k_ffn_gemm<EPI, F32>;
   constexpr int smem = Plan<EPI, F32>::kSmem;

@@ -2,20 +2,26 @@
 // the fifth-generation tensor cores, with the block's activation in their
 // epilogues.
 //
-// Every product is D[n][m] = sum_k A(m, k) B(k, n) with m along the
-// contiguous axis of D: m runs over positions (or, for weight gradients, over
-// a weight's contiguous channels) and lies in the lanes of tensor memory, so
-// that a warp's stores of one n are adjacent.  Operands keep the layout they
-// have in memory: a tile whose m (or n) axis is the contiguous one is staged
+// Every product is D(m, n) = sum_k A(m, k) B(k, n); m lies in the lanes of
+// tensor memory and n in its columns.  Operands keep the layout they have in
+// memory: a tile whose m (or n) axis is the contiguous one is staged
 // "MN-major", otherwise "K-major"; both in 128-byte swizzled shared memory,
-// brought by TMA, whose out-of-range zeros cover every ragged edge.
+// brought by TMA, whose out-of-range zeros cover every ragged edge.  Where m
+// is the contiguous axis of D (positions of [B, C, L] outputs, channels of a
+// weight gradient) a warp's stores of one n are adjacent; the hidden
+// activations, which only these products read, lie the other way, [position]
+// [channel], so that a thread stores its 16 adjacent channels in one
+// instruction.
 //
 // A pair of CTAs computes a 256 x 256 tile (cta_group::2): each holds 128 rows
 // of A, half of B's columns and 128 accumulator lanes.  One warp issues TMA,
 // one (of the leading CTA) the MMAs, eight read the accumulators back.
 // Accumulators are fp32 in tensor memory, two of 256 columns, so that the
-// epilogue of a tile runs under the products of the next (three of 128
-// columns, once, where the epilogue needs G, U and dH together).
+// epilogue of a tile runs under the products of the next.  Where the epilogue
+// needs G, U and dH together a tile has 80 hidden channels: 80 + 80 + 96
+// columns (the pair's MMA wants a multiple of 32) fill one of the two
+// accumulators.  One accumulator of three times 128, and no overlap, took 106
+// instead of the present time at C 256, F 1024 and 32768 positions.
 //
 // fp32 operands come as three bf16 planes (high, middle, low: 24 bits) and
 // every K loop runs over the six plane products that reach 2^-24, the small
@@ -47,7 +53,8 @@ struct Seg {
   int a, b0, b1;             // tensor maps; b1 is the second CTA's B
   int a_mn, b_mn;            // 1: the tile's m (n) axis is contiguous in memory
   int a_batched, b_batched;  // the map's third coordinate follows the batch
-  int ncols;                 // columns over the pair: 256, 128 or 64
+  int ncols;                 // columns over the pair, at most 256
+  int nstep, noff;           // n of a tile, and of the second CTA's part in it
   int acc;                   // first accumulator column
   int clear;                 // starts this accumulator
   int kblocks;               // stages per batch of the K loop
@@ -102,10 +109,9 @@ struct Params {
   int planes;                // 1, or 3 for fp32
   int a_plane, b_plane;      // third-coordinate distance of the planes
   int act;
-  // fp32: the hidden planes [3][n][pitch]
+  // the hidden tensors [plane][batch][position][channel]
   __nv_bfloat16* hid[3];
-  long long hid_plane, hid_rs;
-  int hmap[3];               // bf16: their maps
+  long long hid_plane, hid_bs, hid_rs;
   int* status;
 };
 
@@ -253,60 +259,67 @@ __device__ __forceinline__ uint32_t instruction(int a_mn, int b_mn, int ncols) {
 }
 
 // --------------------------------------------------------------- activation
-template <bool F32>
-__device__ __forceinline__ float exp_of(float x) {
-  return F32 ? expf(x) : __expf(x);
-}
-template <bool F32>
-__device__ __forceinline__ float over(float a, float b) {
-  return F32 ? a / b : __fdividef(a, b);
-}
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f, kLog2e = 1.4426950408889634f;
 
-// act(g)
-template <bool F32, int ACT>
-__device__ __forceinline__ float act_of(float g) {
-  if (ACT) return g * (0.5f + 0.5f * erff(g * kSqrtHalf));
-  // the fast quotient wants a denominator below 2^126; beyond e^87 the result is below 1e-35 anyway
-  return over<F32>(g, 1.f + exp_of<F32>(fminf(-g, 87.f)));
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-// act(g) and act'(g)
-template <bool F32, int ACT>
-__device__ __forceinline__ void act_both(float g, float& a, float& da) {
-  if (ACT) {
-    const float cdf = 0.5f + 0.5f * erff(g * kSqrtHalf);
-    a = g * cdf;
-    da = cdf + g * kInvSqrt2Pi * exp_of<F32>(-0.5f * g * g);
+__device__ __forceinline__ float recip_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 1 / (1 + exp(-g)) of two gates.  bf16: one reciprocal of the product serves
+// both, since the special-function unit (two exponentials and two reciprocals
+// for a pair otherwise) is what the epilogue waits for; exp(-g) is held at
+// 2^60 to keep the product finite, so that gates below -41.6 get 2^-60 for
+// their smaller value.
+template <bool F32>
+__device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
+  if constexpr (F32) {
+    s[0] = recip_fast(1.f + expf(fminf(-g[0], 87.f)));     // off by one unit in the last place at most
+    s[1] = recip_fast(1.f + expf(fminf(-g[1], 87.f)));
   } else {
-    const float s = over<F32>(1.f, 1.f + exp_of<F32>(fminf(-g, 87.f)));
-    a = g * s;
-    da = s * (1.f + g * (1.f - s));
+    const float d0 = 1.f + exp2_fast(fminf(-kLog2e * g[0], 60.f)), d1 = 1.f + exp2_fast(fminf(-kLog2e * g[1], 60.f));
+    const float r = recip_fast(d0 * d1);
+    s[0] = r * d1;
+    s[1] = r * d0;
   }
 }
 
-// H, dG and dU of one position and hidden channel.
+// act(g) u of two hidden channels.
 template <bool F32, int ACT>
-__device__ __forceinline__ void hidden_grads(float g, float u, float d, float (&r)[3]) {
-  float a, da;
-  act_both<F32, ACT>(g, a, da);
-  r[0] = a * u;
-  r[1] = d * u * da;
-  r[2] = d * a;
+__device__ __forceinline__ void hidden2(const float (&g)[2], const float (&u)[2], float (&h)[2]) {
+  float s[2];
+  if constexpr (ACT == 0) sigmoid2<F32>(g, s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) h[i] = g[i] * (ACT ? 0.5f + 0.5f * erff(g[i] * kSqrtHalf) : s[i]) * u[i];
 }
 
-// The activation as a constant of the code that runs over many values: a
-// branch at each of them would keep their exponentials from overlapping.
-template <class Fn>
-__device__ __forceinline__ void with_act(int act, Fn fn) {
-  if (act)
-    fn(std::integral_constant<int, 1>{});
-  else
-    fn(std::integral_constant<int, 0>{});
-}
-
-__device__ __forceinline__ void stage_put(uint32_t addr, float v) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&h)));
+// H, dG and dU of two hidden channels.
+template <bool F32, int ACT>
+__device__ __forceinline__ void hidden_grads2(const float (&g)[2], const float (&u)[2], const float (&d)[2],
+                                              float (&h)[2], float (&dg)[2], float (&du)[2]) {
+  float s[2];
+  if constexpr (ACT == 0) sigmoid2<F32>(g, s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a, da;
+    if constexpr (ACT) {
+      const float cdf = 0.5f + 0.5f * erff(g[i] * kSqrtHalf);
+      a = g[i] * cdf;
+      da = cdf + g[i] * kInvSqrt2Pi * (F32 ? expf(-0.5f * g[i] * g[i]) : exp2_fast(-0.5f * kLog2e * g[i] * g[i]));
+    } else {
+      a = g[i] * s[i];
+      da = s[i] + a * (1.f - s[i]);
+    }
+    h[i] = a * u[i];
+    dg[i] = d[i] * u[i] * da;
+    du[i] = d[i] * a;
+  }
 }
 
 // The bf16 planes of an fp32 value.  Values beyond bf16's largest keep a
@@ -319,10 +332,58 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16& hi, __nv_bfloat16
   lo = __float2bfloat16_rn(r - __bfloat162float(mid));
 }
 
+// Two values' planes, packed plane by plane.
+__device__ __forceinline__ void split3x2(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  __nv_bfloat162 h[3];
+  split3(a, h[0].x, h[1].x, h[2].x);
+  split3(b, h[0].y, h[1].y, h[2].y);
+  hi = *reinterpret_cast<const uint32_t*>(&h[0]);
+  mid = *reinterpret_cast<const uint32_t*>(&h[1]);
+  lo = *reinterpret_cast<const uint32_t*>(&h[2]);
+}
+
+// The activation as a constant of the code that runs over many values: a
+// branch at each of them would keep their exponentials from overlapping.
+template <class Fn>
+__device__ __forceinline__ void with_act(int act, Fn fn) {
+  if (act)
+    fn(std::integral_constant<int, 1>{});
+  else
+    fn(std::integral_constant<int, 0>{});
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 bytes in one store.
+struct alignas(32) Vec32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(HND_G(reinterpret_cast<Vec32*>(p))),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void stage_put(uint32_t addr, float v) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&h)));
+}
+
 // ------------------------------------------------------------------- kernel
 struct Tile {
   int job, split, batch, mt, nt;
 };
+
+// Keeps a value in its register: launch parameters picked by a running index
+// are otherwise read again at each use, a dependent load of some 50 cycles,
+// and the two issuing threads then take longer for a stage than its products.
+__device__ __forceinline__ int pinned(int v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
 
 // Tiles run in groups of eight m tiles over all n tiles, so that the tiles in
 // flight share both operands in L2.
@@ -378,16 +439,17 @@ __device__ __forceinline__ void planes_of(int combo, int& a, int& b) {
 
 template <int EPI, bool F32>
 struct Plan {
-  static constexpr int kBufs = EPI == kEpiGrad && !F32 ? 1 : 2;     // accumulators of 256 columns (or one of 384)
-  // columns of a tile: hidden channels, or columns of D.  fp32 halves them: a
-  // thread holds its columns' sums in registers, 64 to 96 of the 168 it has
-  static constexpr int kCols = (EPI == kEpiOut ? 256 : 128) / (F32 ? 2 : 1);
+  static constexpr int kBufs = 2;                                   // accumulators of 256 columns
   static constexpr int kPiece = F32 ? 2 : 1 << 30;                  // stages added up in tensor memory
-  static constexpr int kStages = EPI == kEpiGrad ? 5 : 6;
-  static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;             // tensors stored together
-  static constexpr int kStoreBufs = EPI == kEpiGrad ? 1 : 2;        // per half of the epilogue
-  static constexpr int kSmem =
-      1024 + kStages * kStage + 2 * kOuts * kStoreBufs * kStoreBytes + 8 * (2 * kStages + 2 * kBufs) + 16;
+  // columns of a tile: hidden channels, or columns of D.  fp32 has fewer: a
+  // thread holds its columns' sums in registers, 64 to 96 of the 168 it has
+  static constexpr int kCols = EPI == kEpiOut ? (F32 ? 128 : 256) : F32 ? 64 : EPI == kEpiGrad ? 80 : 128;
+  static constexpr int kGradCols = F32 ? 64 : 96;                   // columns of dH
+  static constexpr int kStages = EPI == kEpiOut ? 6 : 7;
+  static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;
+  static constexpr int kStoreBufs = 2;                              // of each half of the epilogue (kEpiOut)
+  static constexpr int kStore = EPI == kEpiOut ? 2 * kStoreBufs * kStoreBytes : 0;
+  static constexpr int kSmem = 1024 + kStages * kStage + kStore + 8 * (2 * kStages + 2 * kBufs) + 16;
 };
 
 template <int EPI, bool F32>
@@ -396,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
   const uint32_t base = (s32(hnd_dyn_smem) + 1023) & ~1023u;
   const uint32_t out = base + PL::kStages * kStage;
-  const uint32_t bars = out + 2 * PL::kOuts * PL::kStoreBufs * kStoreBytes;
+  const uint32_t bars = out + PL::kStore;
   const uint32_t full = bars, empty = full + 8 * PL::kStages, accf = empty + 8 * PL::kStages,
                  acce = accf + 8 * PL::kBufs, tmem_slot = acce + 8 * PL::kBufs;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -426,6 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
     // ---- TMA: this CTA's 128 rows of A and its half of B
     if (lane == 0) {
       int st = 0, ph = 0;
+      const uint32_t lead_full = in_leader(full);
       for (int t = pair; ok && t < p.tiles; t += pairs) {
         const Tile ti = tile_of(p, t);
         const Job& j = p.job[ti.job];
@@ -440,34 +503,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
             const CUtensorMap* ma = &p.map[s.a];
             const CUtensorMap* mb = &p.map[rank ? s.b1 : s.b0];
             const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
-            const bool dual = s.b0 != s.b1;
-            const int half_n = s.ncols / 2;
-            const int n0 = dual ? ti.nt * half_n : ti.nt * s.ncols + static_cast<int>(rank) * half_n;
-            // MN-major boxes are 64 wide, also where 32 of them are used
-            const uint32_t bytes = 2 * (kHalf + 2 * kBK * (s.b_mn && half_n < 64 ? 64 : half_n));
+            const int half_n = pinned(s.ncols / 2), n0 = pinned(ti.nt * s.nstep + static_cast<int>(rank) * s.noff);
+            const int a_mn = pinned(s.a_mn), b_mn = pinned(s.b_mn), kblocks = pinned(s.kblocks);
+            const bool long_k = pinned(j.kbatches) > 1;
+            const int abat = pinned(s.a_batched), bbat = pinned(s.b_batched);
+            const int za0 = pa * p.a_plane, zb0 = pb * p.b_plane;
+            // MN-major boxes are 64 wide, also where fewer are used
+            const uint32_t bytes = 2 * (kHalf + 2 * kBK * (b_mn && half_n < 64 ? 64 : half_n));
+            int bat = long_k ? lo / kblocks : ti.batch, k = (long_k ? lo - bat * kblocks : lo) * kBK;
             for (int kb = lo; kb < hi; ++kb) {
               if (!bar_wait(empty + 8 * st, ph ^ 1, p.status)) {
                 ok = false;
                 break;
               }
-              const int kbat = j.kbatches > 1 ? kb / s.kblocks : 0, k = (kb - kbat * s.kblocks) * kBK;
-              const int bat = j.kbatches > 1 ? kbat : ti.batch;
-              const int za = pa * p.a_plane + (s.a_batched ? bat : 0), zb = pb * p.b_plane + (s.b_batched ? bat : 0);
-              const uint32_t sa = base + st * kStage, sb = sa + kHalf, bar = in_leader(full + 8 * st);
+              const int za = za0 + (abat ? bat : 0), zb = zb0 + (bbat ? bat : 0);
+              const uint32_t sa = base + st * kStage, sb = sa + kHalf, bar = lead_full + 8 * st;
               if (rank == 0) bar_expect(full + 8 * st, bytes);
-              if (s.a_mn) {
+              if (a_mn) {
                 tma_load(sa, ma, bar, m0, k, za);
                 tma_load(sa + 8192, ma, bar, m0 + 64, k, za);
               } else {
                 tma_load(sa, ma, bar, k, m0, za);
               }
-              if (s.b_mn) {
+              if (b_mn) {
                 tma_load(sb, mb, bar, n0, k, zb);
                 if (half_n > 64) tma_load(sb + 8192, mb, bar, n0 + 64, k, zb);
               } else {
                 tma_load(sb, mb, bar, k, n0, zb);
               }
               if (++st == PL::kStages) st = 0, ph ^= 1;
+              k += kBK;
+              if (long_k && k == kblocks * kBK) k = 0, ++bat;
             }
           }
         }
@@ -498,8 +564,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
             const Seg& s = p.seg[j.seg0 + si];
             int lo, hi;
             k_piece<PL::kPiece>(j, s, ti.split, pc, lo, hi);
-            const uint32_t id = instruction(s.a_mn, s.b_mn, s.ncols), d = tmem + buf * 256 + s.acc;
-            const uint32_t da = s.a_mn ? 2048 >> 4 : 32 >> 4, db = s.b_mn ? 2048 >> 4 : 32 >> 4;
+            const int a_mn = pinned(s.a_mn), b_mn = pinned(s.b_mn);
+            const uint32_t id = pinned(instruction(a_mn, b_mn, s.ncols)), d = pinned(tmem + buf * 256 + s.acc);
+            const uint32_t da = a_mn ? 2048 >> 4 : 32 >> 4, db = b_mn ? 2048 >> 4 : 32 >> 4;
             bool add = c > 0 || !s.clear;
             for (int kb = lo; kb < hi; ++kb) {
               if (!bar_wait(full + 8 * st, ph, p.status)) {
@@ -508,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
               }
               tmem_fence_after();
               const uint32_t sa = base + st * kStage;
-              const uint64_t a = operand(sa, s.a_mn), b = operand(sa + kHalf, s.b_mn);
+              const uint64_t a = operand(sa, a_mn), b = operand(sa + kHalf, b_mn);
 #pragma unroll
               for (int i = 0; i < kBK / 16; ++i) {
                 mma(d, a + i * da, b + i * db, id, add);
@@ -528,8 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
     const int quad = warp % 4, half = (warp - 2) / 4, row = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const bool issuer = (warp == 2 || warp == 6) && lane == 0;
-    const uint32_t stage = out + half * (PL::kOuts * PL::kStoreBufs * kStoreBytes);
-    int buf = 0, bph = 0, sbuf = 0;
+    const uint32_t stage = out + half * (PL::kStoreBufs * kStoreBytes);
+    int buf = 0, bph = 0, sbuf = 0, turn = half;
     // all four warps of the half go on, or none: they meet at barriers below
     auto arrived = [&] {
       const bool yes = named_all(1 + half, 128, bar_wait(accf + 8 * buf, bph, p.status));
@@ -590,26 +657,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
                     make_float4(sum[0][i], sum[0][i + 1], sum[0][i + 2], sum[0][i + 3]);
           }
         } else {
+          __nv_bfloat16* o = p.hid[0] + m * p.hid_rs + n0;
+          const long long apart[3] = {0, p.hid[1] - p.hid[0], p.hid[2] - p.hid[0]};
           with_act(p.act, [&](auto kind) {
-          constexpr int ACT = decltype(kind)::value;
+            constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            float r[PL::kOuts];
-            if constexpr (EPI == kEpiGrad) {
-              hidden_grads<true, ACT>(sum[0][i], sum[1][i], sum[2][i], r);
-            } else {
-              r[0] = act_of<true, ACT>(sum[0][i]) * sum[1][i];
-            }
-            if (live && n0 + i < j.N)
+            for (int i0 = 0; i0 < W; i0 += 8) {
+              uint32_t w[PL::kOuts][3][4];
 #pragma unroll
-              for (int q = 0; q < PL::kOuts; ++q) {
-                __nv_bfloat16 h[3];
-                split3(r[q], h[0], h[1], h[2]);
-                __nv_bfloat16* o = p.hid[q] + (n0 + i) * p.hid_rs + m;
+              for (int i = 0; i < 8; i += 2) {
+                const float g[2] = {sum[0][i0 + i], sum[0][i0 + i + 1]}, u[2] = {sum[1][i0 + i], sum[1][i0 + i + 1]};
+                float r[3][2];
+                if constexpr (EPI == kEpiGrad) {
+                  const float d[2] = {sum[2][i0 + i], sum[2][i0 + i + 1]};
+                  hidden_grads2<true, ACT>(g, u, d, r[0], r[1], r[2]);
+                } else {
+                  hidden2<true, ACT>(g, u, r[0]);
+                }
 #pragma unroll
-                for (int k = 0; k < 3; ++k) *HND_G(o + k * p.hid_plane) = h[k];
+                for (int q = 0; q < PL::kOuts; ++q) split3x2(r[q][0], r[q][1], w[q][0][i / 2], w[q][1][i / 2], w[q][2][i / 2]);
               }
-          }
+              if (live && n0 + i0 < j.N)
+#pragma unroll
+                for (int q = 0; q < PL::kOuts; ++q)
+#pragma unroll
+                  for (int k = 0; k < 3; ++k)
+                    *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
+                        make_uint4(w[q][k][0], w[q][k][1], w[q][k][2], w[q][k][3]);
+            }
           });
         }
       } else {
@@ -652,62 +727,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
                 if (live && n0 + i < j.N) {
                   uint32_t w[4];
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * q]),
-                                                                   __uint_as_float(v[i + 2 * q + 1]));
-                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
-                  }
+                  for (int q = 0; q < 4; ++q) w[q] = pack2(__uint_as_float(v[i + 2 * q]), __uint_as_float(v[i + 2 * q + 1]));
                   *HND_G(reinterpret_cast<uint4*>(o + i)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
           }
         } else {
-          // hidden channels n of this half: [64 half, 64 half + 64) of the tile's 128
-          constexpr int W = EPI == kEpiGrad ? 16 : 32;
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            const int nc = half * 64 + c0, n0 = ti.nt * 128 + nc;
-            const uint32_t sb = stage + sbuf * kStoreBytes;
-            if (issuer) store_wait_read<PL::kStoreBufs - 1>();
-            named_sync(1 + half, 128);
+          // the tile's hidden channels in pieces of W, taken by the two halves in turn (of 5 pieces each half
+          // takes 3 in every second tile)
+          constexpr int W = EPI == kEpiGrad ? 16 : 32, kPieces = PL::kCols / W;
+          __nv_bfloat16* o = p.hid[0] + ti.batch * p.hid_bs + m * p.hid_rs + ti.nt * PL::kCols;
+          const long long apart[3] = {0, p.hid[1] - p.hid[0], p.hid[2] - p.hid[0]};
+          const int left = static_cast<int>(j.N) - ti.nt * PL::kCols;      // channels of the tile that exist
+          for (int k = turn; k < kPieces; k += 2) {
+            uint32_t g[W], u[W], d[EPI == kEpiGrad ? W : 1];
+            tmem_load(g, acc + k * W);
+            tmem_load(u, acc + PL::kCols + k * W);
+            if constexpr (EPI == kEpiGrad) tmem_load(d, acc + 2 * PL::kCols + k * W);
+            tmem_wait_load();
+            if (k + 2 >= kPieces) release();
+            with_act(p.act, [&](auto kind) {
+              constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-            for (int w0 = 0; w0 < 32; w0 += W) {
-              uint32_t g[W], u[W], d[EPI == kEpiGrad ? W : 1];
-              tmem_load(g, acc + nc + w0);
-              tmem_load(u, acc + 128 + nc + w0);
-              if constexpr (EPI == kEpiGrad) tmem_load(d, acc + 256 + nc + w0);
-              tmem_wait_load();
-              if (c0 + w0 == 64 - W) release();
-              with_act(p.act, [&](auto kind) {
-                constexpr int ACT = decltype(kind)::value;
+              for (int i0 = 0; i0 < W; i0 += 16) {
+                uint32_t w[PL::kOuts][8];
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                  const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
-                  float r[PL::kOuts];
-                  if constexpr (EPI == kEpiGrad)
-                    hidden_grads<false, ACT>(gv, uv, __uint_as_float(d[i]), r);
-                  else
-                    r[0] = act_of<false, ACT>(gv) * uv;
+                for (int i = i0; i < i0 + 16; i += 2) {
+                  const float gv[2] = {__uint_as_float(g[i]), __uint_as_float(g[i + 1])};
+                  const float uv[2] = {__uint_as_float(u[i]), __uint_as_float(u[i + 1])};
+                  float r[3][2];
+                  if constexpr (EPI == kEpiGrad) {
+                    const float dv[2] = {__uint_as_float(d[i]), __uint_as_float(d[i + 1])};
+                    hidden_grads2<false, ACT>(gv, uv, dv, r[0], r[1], r[2]);
+                  } else {
+                    hidden2<false, ACT>(gv, uv, r[0]);
+                  }
 #pragma unroll
-                  for (int q = 0; q < PL::kOuts; ++q)
-                    stage_put(sb + q * (PL::kStoreBufs * kStoreBytes) + (w0 + i) * 256 + row * 2, r[q]);
+                  for (int q = 0; q < PL::kOuts; ++q) w[q][(i - i0) / 2] = pack2(r[q][0], r[q][1]);
                 }
-              });
-            }
-            fence_async();
-            named_sync(1 + half, 128);
-            if (issuer) {
-              if (m0 < j.M && n0 < j.N)
+                if (live && k * W + i0 < left)
 #pragma unroll
-                for (int q = 0; q < PL::kOuts; ++q)
-                  tma_store(&p.map[p.hmap[q]], sb + q * (PL::kStoreBufs * kStoreBytes), m0, n0, ti.batch);
-              store_commit();
-            }
-            sbuf = (sbuf + 1) % PL::kStoreBufs;
+                  for (int q = 0; q < PL::kOuts; ++q) store32(o + apart[q] + k * W + i0, w[q]);
+              }
+            });
           }
+          if (kPieces % 2) turn ^= 1;
         }
       }
     }
-    if (issuer) store_wait_read<0>();
+    if (EPI == kEpiOut && issuer) store_wait_read<0>();
   }
   __syncwarp();
   tmem_fence_before();

@@ -68,7 +68,7 @@ struct Layout {
   int planes;
   long long batches, Lx;     // of the position axis as the products see it
   long long pitch;           // of packed rows (token: of a position's channels)
-  long long hpitch;          // of the hidden rows
+  long long hpitch;          // of a position's hidden channels
   size_t x, dy, w, hid, part, bytes;
   long long act_plane, w_plane, hid_plane;   // elements
   int splits;
@@ -103,7 +103,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   l.batches = merged ? 1 : a.B;
   l.Lx = merged ? T : a.L;
   l.pitch = l.token ? a.C : up(T, 8);
-  l.hpitch = up(l.Lx, 8);
+  l.hpitch = up(a.F, 16);      // whole 32-byte stores
   const bool copied = l.packed || !a.bf16;
   size_t at = 0;
   auto take = [&](long long elements, size_t size) {
@@ -113,7 +113,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   };
   l.act_plane = l.token ? T * a.C : a.C * l.pitch;
   l.w_plane = a.C * a.F;
-  l.hid_plane = l.batches * a.F * l.hpitch;
+  l.hid_plane = l.batches * l.Lx * l.hpitch;
   if (copied) l.x = take(l.planes * l.act_plane, 2);
   if (copied && backward) l.dy = take(l.planes * l.act_plane, 2);
   if (!a.bf16) l.w = take(9 * l.w_plane, 2);
@@ -217,7 +217,8 @@ template <bool F32>
 struct Ffn {
   using TT = typename std::conditional<F32, float, bf16>::type;
   // columns of a tile: hidden channels, and columns of the other products
-  static constexpr int hn = Plan<kEpiHidden, F32>::kCols, on = Plan<kEpiOut, F32>::kCols;
+  using PG = Plan<kEpiGrad, F32>;
+  static constexpr int hn = Plan<kEpiHidden, F32>::kCols, gn = PG::kCols, on = Plan<kEpiOut, F32>::kCols;
   const FfnArgs& a;
   const Layout l;
   const long long T;
@@ -235,7 +236,7 @@ struct Ffn {
       for (int i = 0; i < 3; ++i) w[i] = wsb(l.w) + 3 * i * l.w_plane;
     wg = weight(w[0], a.F, a.C), wu = weight(w[1], a.F, a.C), wd = weight(w[2], a.C, a.F);
     for (int i = 0; i < 3; ++i)
-      hid[i] = Mat{wsb(l.hid) + i * l.planes * l.hid_plane, l.Lx, a.F, l.batches * l.planes, l.hpitch, a.F * l.hpitch};
+      hid[i] = Mat{wsb(l.hid) + i * l.planes * l.hid_plane, a.F, l.Lx, l.batches * l.planes, l.hpitch, l.Lx * l.hpitch};
   }
   Mat activation(const void* p) const {
     if (l.token) return Mat{p, a.C, T, l.planes, a.C, l.act_plane};
@@ -278,8 +279,17 @@ struct Ffn {
   // activations as the rows of a product (m = positions): the position axis
   // is contiguous, except token-major, where the channels are
   int positions(Launch& n, const Mat& m) const { return l.token ? n.km(m) : n.mn(m); }
-  Seg data_seg(int ma, int mb0, int mb1, bool a_mn, bool b_mn, int ncols, int acc, int clear, long long depth) const {
-    return Seg{ma, mb0, mb1, a_mn, b_mn, l.batches > 1, 0, ncols, acc, clear, static_cast<int>(cdiv(depth, kBK))};
+  Seg data_seg(int ma, int mb, bool a_mn, bool b_mn, int ncols, int acc, int clear, long long depth) const {
+    return Seg{ma,  mb,    mb, a_mn, b_mn, l.batches > 1, 0, ncols, ncols, ncols / 2,
+               acc, clear, static_cast<int>(cdiv(depth, kBK))};
+  }
+  // G and U of `cols` hidden channels side by side: the first CTA brings Wg, the second Wu
+  Seg gates_seg(Launch& n, int cols) const {
+    Seg s = data_seg(positions(n, x), n.km(wg, cols), !l.token, false, 2 * cols, 0, 1, a.C);
+    s.b1 = n.km(wu, cols);
+    s.nstep = cols;
+    s.noff = 0;
+    return s;
   }
   Job data_job(int nseg, long long N, int per_tile) const {
     Job j{};
@@ -293,11 +303,9 @@ struct Ffn {
     return j;
   }
   void hidden_out(Launch& n, int count) const {
-    for (int i = 0; i < count; ++i) {
-      n.p.hid[i] = static_cast<bf16*>(const_cast<void*>(hid[i].p));
-      if (!F32) n.p.hmap[i] = n.store(hid[i]);
-    }
+    for (int i = 0; i < count; ++i) n.p.hid[i] = static_cast<bf16*>(const_cast<void*>(hid[i].p));
     n.p.hid_plane = l.hid_plane;
+    n.p.hid_bs = l.Lx * l.hpitch;
     n.p.hid_rs = l.hpitch;
   }
   // y or dx: back to the activations' own layout
@@ -321,13 +329,12 @@ struct Ffn {
     cudaError_t e;
     if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_weights()) != cudaSuccess) return e;
     Launch h = start();
-    h.p.seg[0] = data_seg(positions(h, x), h.km(wg, hn), h.km(wu, hn), !l.token, false, 2 * hn, 0, 1, a.C);
+    h.p.seg[0] = gates_seg(h, hn);
     hidden_out(h, 1);
     h.job(data_job(1, a.F, hn));
     if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
     Launch y = start();
-    const int m = y.km(wd, on / 2);
-    y.p.seg[0] = data_seg(y.mn(hid[0]), m, m, true, false, on, 0, 1, a.F);
+    y.p.seg[0] = data_seg(y.km(hid[0]), y.km(wd, on / 2), false, false, on, 0, 1, a.F);
     Job j = data_job(1, a.C, on);
     activation_out(y, j, a.y);
     y.job(j);
@@ -341,17 +348,16 @@ struct Ffn {
       return e;
     // H, dG, dU
     Launch h = start();
-        h.p.seg[0] = data_seg(positions(h, x), h.km(wg, hn), h.km(wu, hn), !l.token, false, 2 * hn, 0, 1, a.C);
-    const int md = h.mn(wd);
-    h.p.seg[1] = data_seg(positions(h, dy), md, md, !l.token, true, hn, 2 * hn, 1, a.C);
+        h.p.seg[0] = gates_seg(h, gn);
+    h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, PG::kGradCols, 2 * gn, 1, a.C);
+    h.p.seg[1].nstep = gn;
     hidden_out(h, 3);
-    h.job(data_job(2, a.F, hn));
+    h.job(data_job(2, a.F, gn));
     if ((e = run<kEpiGrad, F32>(h, a.stream)) != cudaSuccess) return e;
     // dX
     Launch d = start();
-    const int mg = d.mn(wg), mu = d.mn(wu);
-    d.p.seg[0] = data_seg(d.mn(hid[1]), mg, mg, true, true, on, 0, 1, a.F);
-    d.p.seg[1] = data_seg(d.mn(hid[2]), mu, mu, true, true, on, 0, 0, a.F);
+    d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1, a.F);
+    d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0, a.F);
     Job j = data_job(2, a.C, on);
     activation_out(d, j, a.dx);
     d.job(j);
@@ -361,10 +367,13 @@ struct Ffn {
     const bool batched = l.batches > 1;
     const int stages = static_cast<int>(cdiv(l.Lx, kBK));
     const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, on / 2);
-    const int mh = w.km(hid[0]), mdg = w.km(hid[1], on / 2), mdu = w.km(hid[2], on / 2);
-    w.p.seg[0] = Seg{mx, mdg, mdg, l.token, 0, batched, batched, on, 0, 1, stages};
-    w.p.seg[1] = Seg{mx, mdu, mdu, l.token, 0, batched, batched, on, 0, 1, stages};
-    w.p.seg[2] = Seg{mh, mdy, mdy, 0, l.token, batched, batched, on, 0, 1, stages};
+    const int mh = w.mn(hid[0]), mdg = w.mn(hid[1]), mdu = w.mn(hid[2]);
+    auto seg = [&](int ma, int mb, int a_mn, int b_mn) {
+      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 1, stages};
+    };
+    w.p.seg[0] = seg(mx, mdg, l.token, 1);
+    w.p.seg[1] = seg(mx, mdu, l.token, 1);
+    w.p.seg[2] = seg(mh, mdy, 1, l.token);
     void* out[3] = {a.dwg, a.dwu, a.dwd};
     float* part = reinterpret_cast<float*>(ws(l.part));
     for (int i = 0; i < 3; ++i) {

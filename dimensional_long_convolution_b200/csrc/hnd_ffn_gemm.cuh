@@ -134,6 +134,12 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -485,8 +491,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
 
   bool ok = true;
   if (warp == 0) {
-    // ---- TMA: this CTA's 128 rows of A and its half of B
-    if (lane == 0) {
+    // ---- TMA: this CTA's 128 rows of A and its half of B.  The warp goes
+    // through the loop as one and a single lane issues: under a branch on the
+    // lane every operand of a copy would first have to be made uniform.
+    const bool lead = elected();
+    {
       int st = 0, ph = 0;
       const uint32_t lead_full = in_leader(full);
       for (int t = pair; ok && t < p.tiles; t += pairs) {
@@ -518,19 +527,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
               }
               const int za = za0 + (abat ? bat : 0), zb = zb0 + (bbat ? bat : 0);
               const uint32_t sa = base + st * kStage, sb = sa + kHalf, bar = lead_full + 8 * st;
-              if (rank == 0) bar_expect(full + 8 * st, bytes);
-              if (a_mn) {
-                tma_load(sa, ma, bar, m0, k, za);
-                tma_load(sa + 8192, ma, bar, m0 + 64, k, za);
-              } else {
-                tma_load(sa, ma, bar, k, m0, za);
+              if (lead) {
+                if (rank == 0) bar_expect(full + 8 * st, bytes);
+                if (a_mn) {
+                  tma_load(sa, ma, bar, m0, k, za);
+                  tma_load(sa + 8192, ma, bar, m0 + 64, k, za);
+                } else {
+                  tma_load(sa, ma, bar, k, m0, za);
+                }
+                if (b_mn) {
+                  tma_load(sb, mb, bar, n0, k, zb);
+                  if (half_n > 64) tma_load(sb + 8192, mb, bar, n0 + 64, k, zb);
+                } else {
+                  tma_load(sb, mb, bar, k, n0, zb);
+                }
               }
-              if (b_mn) {
-                tma_load(sb, mb, bar, n0, k, zb);
-                if (half_n > 64) tma_load(sb + 8192, mb, bar, n0 + 64, k, zb);
-              } else {
-                tma_load(sb, mb, bar, k, n0, zb);
-              }
+              __syncwarp();
               if (++st == PL::kStages) st = 0, ph ^= 1;
               k += kBK;
               if (long_k && k == kblocks * kBK) k = 0, ++bat;
@@ -545,8 +557,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
       }
     }
   } else if (warp == 1) {
-    // ---- MMA: one thread of the leading CTA
-    if (rank == 0 && lane == 0) {
+    // ---- MMA: one lane of the leading CTA's warp
+    const bool lead = elected();
+    if (rank == 0) {
       int st = 0, ph = 0, buf = 0, bph = 0;
       const bool alike = p.jobs == 1 && p.job[0].splits == 1;      // every tile has the same K loop
       for (int t = pair; ok && t < p.tiles; t += pairs) {
@@ -576,16 +589,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
               tmem_fence_after();
               const uint32_t sa = base + st * kStage;
               const uint64_t a = operand(sa, a_mn), b = operand(sa + kHalf, b_mn);
+              if (lead) {
 #pragma unroll
-              for (int i = 0; i < kBK / 16; ++i) {
-                mma(d, a + i * da, b + i * db, id, add);
-                add = true;
+                for (int i = 0; i < kBK / 16; ++i) mma(d, a + i * da, b + i * db, id, add || i > 0);
+                mma_commit(empty + 8 * st);
               }
-              mma_commit(empty + 8 * st);
+              __syncwarp();
+              add = true;
               if (++st == PL::kStages) st = 0, ph ^= 1;
             }
           }
-        mma_commit(accf + 8 * buf);
+        if (lead) mma_commit(accf + 8 * buf);
+        __syncwarp();
         if (++buf == PL::kBufs) buf = 0, bph ^= 1;
         }
       }

@@ -42,7 +42,7 @@
 namespace hnd {
 namespace ffn {
 
-constexpr int kThreads = 320;          // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kThreads = 352;          // a warp for A's copies, one for the MMAs, 8 of epilogue, one for B's copies
 constexpr int kBK = 64;                // depth of a stage
 constexpr int kHalf = 128 * kBK * 2;   // bytes of A (and of B) per CTA and stage
 constexpr int kStage = 2 * kHalf;
@@ -57,7 +57,6 @@ struct Seg {
   int nstep, noff;           // n of a tile, and of the second CTA's part in it
   int acc;                   // first accumulator column
   int clear;                 // starts this accumulator
-  int kblocks;               // stages per batch of the K loop
 };
 
 enum OutKind {
@@ -90,7 +89,8 @@ inline Div make_div(uint32_t d) {
 struct Job {
   int seg0, nseg;
   int batches, mt, nt, splits;
-  int kbatches;              // batches of the K loop (weight gradients)
+  int kbatches, kblocks;     // the K loop: batches (of weight gradients), stages of each
+  int kper;                  // stages of a split
   Div per, group8, mdiv;     // tiles of a split, of eight m tiles; mt
   long long M, N;            // extents of D
   int kind, map;             // how D leaves, and the map of kOutTma
@@ -380,61 +380,69 @@ __device__ __forceinline__ void stage_put(uint32_t addr, float v) {
 
 // ------------------------------------------------------------------- kernel
 struct Tile {
-  int job, split, batch, mt, nt;
+  int split, batch, mt, nt;
 };
 
 // Keeps a value in its register: launch parameters picked by a running index
 // are otherwise read again at each use, a dependent load of some 50 cycles,
-// and the two issuing threads then take longer for a stage than its products.
+// and the issuing warps then take longer for a stage than its products.
 __device__ __forceinline__ int pinned(int v) {
   asm volatile("" : "+r"(v));
   return v;
 }
+__device__ __forceinline__ Div pinned(const Div& d) {
+  return Div{static_cast<uint32_t>(pinned(static_cast<int>(d.d))), static_cast<uint32_t>(pinned(static_cast<int>(d.mul))),
+             static_cast<uint32_t>(pinned(static_cast<int>(d.shift)))};
+}
 
+// A warp's way through the tiles: the current job's shape in registers.
 // Tiles run in groups of eight m tiles over all n tiles, so that the tiles in
 // flight share both operands in L2.
-__device__ __forceinline__ Tile tile_of(const Params& p, int t) {
-  Tile r{};
-  for (; r.job < p.jobs - 1; ++r.job) {
-    const Job& j = p.job[r.job];
-    const int n = j.batches * j.mt * j.nt * j.splits;
-    if (t < n) break;
-    t -= n;
+struct Walk {
+  int job = -1, begin = 0, end = 0;
+  int mm, mt, splits, stages, kper;
+  Div per, group8, mdiv;
+
+  __device__ __forceinline__ void seek(const Params& p, int t) {      // t never falls
+    while (t >= end) {
+      const Job& j = p.job[++job];
+      mt = pinned(j.mt);
+      mm = pinned(j.batches * j.mt);
+      splits = pinned(j.splits);
+      stages = pinned(j.kbatches * j.kblocks);
+      kper = pinned(j.kper);
+      per = pinned(j.per), group8 = pinned(j.group8), mdiv = pinned(j.mdiv);
+      begin = end;
+      end += static_cast<int>(per.d) * splits;
+    }
   }
-  const Job& j = p.job[r.job];
-  const int mm = j.batches * j.mt;
-  r.split = j.per.quot(t);
-  t -= r.split * static_cast<int>(j.per.d);
-  const int g = j.group8.quot(t), rows = min(8, mm - 8 * g);
-  t -= g * static_cast<int>(j.group8.d);
-  r.nt = rows == 8 ? t >> 3 : t / rows;
-  const int m = 8 * g + t - r.nt * rows;
-  r.batch = j.mdiv.quot(m);
-  r.mt = m - r.batch * j.mt;
-  return r;
-}
-
-// The stages [lo, hi) of a segment that a split takes.
-__device__ __forceinline__ void k_range(const Job& j, const Seg& s, int split, int& lo, int& hi) {
-  const int all = j.kbatches * s.kblocks, per = (all + j.splits - 1) / j.splits;
-  lo = min(all, split * per);
-  hi = min(all, lo + per);
-}
-
-// fp32: the pieces a tile's K loop is added up in, and one of them.
+  __device__ __forceinline__ int split(int t) const { return splits > 1 ? per.quot(t - begin) : 0; }
+  __device__ __forceinline__ Tile tile(int t) const {
+    Tile r{};
+    r.split = split(t);
+    t -= begin + r.split * static_cast<int>(per.d);
+    const int g = group8.quot(t), rows = min(8, mm - 8 * g);
+    t -= g * static_cast<int>(group8.d);
+    r.nt = rows == 8 ? t >> 3 : t / rows;
+    const int m = 8 * g + t - r.nt * rows;
+    r.batch = mdiv.quot(m);
+    r.mt = m - r.batch * mt;
+    return r;
+  }
+  // The stages [lo, hi) of a split, and how many pieces of PIECE they are.
+  __device__ __forceinline__ void range(int split, int& lo, int& hi) const {
+    lo = min(stages, split * kper);
+    hi = min(stages, lo + kper);
+  }
+};
 template <int PIECE>
-__device__ __forceinline__ int pieces_of(const Params& p, const Job& j, int split) {
-  int lo, hi;
-  k_range(j, p.seg[j.seg0], split, lo, hi);
+__device__ __forceinline__ int pieces_of(int lo, int hi) {
   return PIECE < 1 << 30 ? (hi - lo + PIECE - 1) / PIECE : 1;
 }
-template <int PIECE>
-__device__ __forceinline__ void k_piece(const Job& j, const Seg& s, int split, int piece, int& lo, int& hi) {
-  k_range(j, s, split, lo, hi);
-  if (PIECE < 1 << 30) {
-    lo += piece * PIECE;
-    hi = min(hi, lo + PIECE);
-  }
+
+// Waits with the whole warp: all lanes go on or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, status));
 }
 
 // Plane products of fp32 operands, the smallest first.
@@ -490,118 +498,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
 
   bool ok = true;
-  if (warp == 0) {
-    // ---- TMA: this CTA's 128 rows of A and its half of B.  The warp goes
-    // through the loop as one and a single lane issues: under a branch on the
-    // lane every operand of a copy would first have to be made uniform.
-    const bool lead = elected();
-    {
-      int st = 0, ph = 0;
-      const uint32_t lead_full = in_leader(full);
-      for (int t = pair; ok && t < p.tiles; t += pairs) {
-        const Tile ti = tile_of(p, t);
-        const Job& j = p.job[ti.job];
-        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
-        for (int pc = 0; ok && pc < pieces * combos; ++pc) {
-          int pa = 0, pb = 0;
-          if (F32) planes_of(pc % combos, pa, pb);
-          for (int si = 0; ok && si < j.nseg; ++si) {
-            const Seg& s = p.seg[j.seg0 + si];
-            int lo, hi;
-            k_piece<PL::kPiece>(j, s, ti.split, pc / combos, lo, hi);
-            const CUtensorMap* ma = &p.map[s.a];
-            const CUtensorMap* mb = &p.map[rank ? s.b1 : s.b0];
-            const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
-            const int half_n = pinned(s.ncols / 2), n0 = pinned(ti.nt * s.nstep + static_cast<int>(rank) * s.noff);
-            const int a_mn = pinned(s.a_mn), b_mn = pinned(s.b_mn), kblocks = pinned(s.kblocks);
-            const bool long_k = pinned(j.kbatches) > 1;
-            const int abat = pinned(s.a_batched), bbat = pinned(s.b_batched);
-            const int za0 = pa * p.a_plane, zb0 = pb * p.b_plane;
-            // MN-major boxes are 64 wide, also where fewer are used
-            const uint32_t bytes = 2 * (kHalf + 2 * kBK * (b_mn && half_n < 64 ? 64 : half_n));
-            int bat = long_k ? lo / kblocks : ti.batch, k = (long_k ? lo - bat * kblocks : lo) * kBK;
-            for (int kb = lo; kb < hi; ++kb) {
-              if (!bar_wait(empty + 8 * st, ph ^ 1, p.status)) {
-                ok = false;
-                break;
+  if (warp == 0 || warp == kThreads / 32 - 1) {
+    // ---- TMA: this CTA's 128 rows of A (first warp) and its part of B (last
+    // warp).  A warp goes through the loop as one and a single lane issues:
+    // under a branch on the lane every operand of a copy would first have to
+    // be made uniform.
+    const bool lead = elected(), is_b = warp != 0;
+    int st = 0, ph = 0;
+    const uint32_t lead_full = in_leader(full);
+    Walk walk;
+    int job = -1, nseg = 0, kblocks = 0, mn[2], half_n[2], step[2], off[2], batched[2];
+    uint32_t bytes[2];
+    const CUtensorMap* map[2];
+    bool long_k = false;
+    for (int t = pair; ok && t < p.tiles; t += pairs) {
+      walk.seek(p, t);
+      if (walk.job != job) {
+        job = walk.job;
+        const Job& j = p.job[job];
+        nseg = pinned(j.nseg);
+        kblocks = pinned(j.kblocks);
+        long_k = pinned(j.kbatches) > 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Seg& s = p.seg[j.seg0 + (i < nseg ? i : 0)];
+          mn[i] = pinned(is_b ? s.b_mn : s.a_mn);
+          half_n[i] = pinned(is_b ? s.ncols / 2 : 128);
+          step[i] = pinned(is_b ? s.nstep : 256);
+          off[i] = pinned(static_cast<int>(rank) * (is_b ? s.noff : 128));
+          batched[i] = pinned(is_b ? s.b_batched : s.a_batched);
+          // MN-major boxes are 64 wide, also where fewer are used
+          bytes[i] = pinned(2 * (kHalf + 2 * kBK * (s.b_mn && s.ncols < 128 ? 64 : s.ncols / 2)));
+          map[i] = &p.map[pinned(is_b ? (rank ? s.b1 : s.b0) : s.a)];
+        }
+      }
+      const Tile ti = walk.tile(t);
+      int lo, hi;
+      walk.range(ti.split, lo, hi);
+      const int pieces = pieces_of<PL::kPiece>(lo, hi);
+      for (int pc = 0; ok && pc < pieces * combos; ++pc) {
+        int plane = 0;
+        if (F32) {
+          int pa, pb;
+          planes_of(pc % combos, pa, pb);
+          plane = is_b ? pb * p.b_plane : pa * p.a_plane;
+        }
+        const int from = F32 ? lo + pc / combos * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= nseg) continue;
+          const int r0 = (is_b ? ti.nt : ti.mt) * step[i] + off[i];
+          int bat = long_k ? from / kblocks : ti.batch, k = (long_k ? from - bat * kblocks : from) * kBK;
+          for (int kb = from; ok && kb < to; ++kb) {
+            if (!(ok = warp_wait(empty + 8 * st, ph ^ 1, p.status))) break;
+            const int z = plane + (batched[i] ? bat : 0);
+            const uint32_t dst = base + st * kStage + (is_b ? kHalf : 0), bar = lead_full + 8 * st;
+            if (lead) {
+              if (rank == 0 && !is_b) bar_expect(full + 8 * st, bytes[i]);
+              if (mn[i]) {
+                tma_load(dst, map[i], bar, r0, k, z);
+                if (half_n[i] > 64) tma_load(dst + 8192, map[i], bar, r0 + 64, k, z);
+              } else {
+                tma_load(dst, map[i], bar, k, r0, z);
               }
-              const int za = za0 + (abat ? bat : 0), zb = zb0 + (bbat ? bat : 0);
-              const uint32_t sa = base + st * kStage, sb = sa + kHalf, bar = lead_full + 8 * st;
-              if (lead) {
-                if (rank == 0) bar_expect(full + 8 * st, bytes);
-                if (a_mn) {
-                  tma_load(sa, ma, bar, m0, k, za);
-                  tma_load(sa + 8192, ma, bar, m0 + 64, k, za);
-                } else {
-                  tma_load(sa, ma, bar, k, m0, za);
-                }
-                if (b_mn) {
-                  tma_load(sb, mb, bar, n0, k, zb);
-                  if (half_n > 64) tma_load(sb + 8192, mb, bar, n0 + 64, k, zb);
-                } else {
-                  tma_load(sb, mb, bar, k, n0, zb);
-                }
-              }
-              __syncwarp();
-              if (++st == PL::kStages) st = 0, ph ^= 1;
-              k += kBK;
-              if (long_k && k == kblocks * kBK) k = 0, ++bat;
             }
+            __syncwarp();
+            if (++st == PL::kStages) st = 0, ph ^= 1;
+            k += kBK;
+            if (long_k && k == kblocks * kBK) k = 0, ++bat;
           }
         }
       }
-      if (!ok) {   // copies in flight land before the shared memory goes: they take microseconds
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 20000000ull) {
-        }
+    }
+    if (!ok) {   // copies in flight land before the shared memory goes: they take microseconds
+      const uint64_t t0 = now_ns();
+      while (now_ns() - t0 < 20000000ull) {
       }
     }
   } else if (warp == 1) {
     // ---- MMA: one lane of the leading CTA's warp
     const bool lead = elected();
     if (rank == 0) {
-      int st = 0, ph = 0, buf = 0, bph = 0;
-      const bool alike = p.jobs == 1 && p.job[0].splits == 1;      // every tile has the same K loop
+      int st = 0, ph = 0, buf = 0, bph = 0, job = -1, nseg = 0, a_mn[2], b_mn[2], acc[2], clear[2];
+      uint32_t id[2];
+      Walk walk;
       for (int t = pair; ok && t < p.tiles; t += pairs) {
-        const Tile ti = alike ? Tile{} : tile_of(p, t);
-        const Job& j = p.job[ti.job];
-        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
-        for (int pc = 0; ok && pc < pieces; ++pc) {
-        if (!bar_wait(acce + 8 * buf, bph ^ 1, p.status)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
-        for (int c = 0; ok && c < combos; ++c)
-          for (int si = 0; ok && si < j.nseg; ++si) {
-            const Seg& s = p.seg[j.seg0 + si];
-            int lo, hi;
-            k_piece<PL::kPiece>(j, s, ti.split, pc, lo, hi);
-            const int a_mn = pinned(s.a_mn), b_mn = pinned(s.b_mn);
-            const uint32_t id = pinned(instruction(a_mn, b_mn, s.ncols)), d = pinned(tmem + buf * 256 + s.acc);
-            const uint32_t da = a_mn ? 2048 >> 4 : 32 >> 4, db = b_mn ? 2048 >> 4 : 32 >> 4;
-            bool add = c > 0 || !s.clear;
-            for (int kb = lo; kb < hi; ++kb) {
-              if (!bar_wait(full + 8 * st, ph, p.status)) {
-                ok = false;
-                break;
-              }
-              tmem_fence_after();
-              const uint32_t sa = base + st * kStage;
-              const uint64_t a = operand(sa, a_mn), b = operand(sa + kHalf, b_mn);
-              if (lead) {
+        walk.seek(p, t);
+        if (walk.job != job) {
+          job = walk.job;
+          const Job& j = p.job[job];
+          nseg = pinned(j.nseg);
 #pragma unroll
-                for (int i = 0; i < kBK / 16; ++i) mma(d, a + i * da, b + i * db, id, add || i > 0);
-                mma_commit(empty + 8 * st);
-              }
-              __syncwarp();
-              add = true;
-              if (++st == PL::kStages) st = 0, ph ^= 1;
-            }
+          for (int i = 0; i < 2; ++i) {
+            const Seg& s = p.seg[j.seg0 + (i < nseg ? i : 0)];
+            a_mn[i] = pinned(s.a_mn), b_mn[i] = pinned(s.b_mn);
+            acc[i] = pinned(s.acc), clear[i] = pinned(s.clear);
+            id[i] = pinned(instruction(s.a_mn, s.b_mn, s.ncols));
           }
-        if (lead) mma_commit(accf + 8 * buf);
-        __syncwarp();
-        if (++buf == PL::kBufs) buf = 0, bph ^= 1;
+        }
+        int lo, hi;
+        walk.range(walk.split(t), lo, hi);
+        const int pieces = pieces_of<PL::kPiece>(lo, hi);
+        for (int pc = 0; ok && pc < pieces; ++pc) {
+          if (!(ok = warp_wait(acce + 8 * buf, bph ^ 1, p.status))) break;
+          tmem_fence_after();
+          const int from = F32 ? lo + pc * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
+          for (int c = 0; ok && c < combos; ++c)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (i >= nseg) continue;
+              const uint32_t d = tmem + buf * 256 + acc[i];
+              const uint32_t da = a_mn[i] ? 2048 >> 4 : 32 >> 4, db = b_mn[i] ? 2048 >> 4 : 32 >> 4;
+              bool add = c > 0 || !clear[i];
+              for (int kb = from; ok && kb < to; ++kb) {
+                if (!(ok = warp_wait(full + 8 * st, ph, p.status))) break;
+                tmem_fence_after();
+                const uint32_t sa = base + st * kStage;
+                const uint64_t a = operand(sa, a_mn[i]), b = operand(sa + kHalf, b_mn[i]);
+                if (lead) {
+#pragma unroll
+                  for (int q = 0; q < kBK / 16; ++q) mma(d, a + q * da, b + q * db, id[i], add || q > 0);
+                  mma_commit(empty + 8 * st);
+                }
+                __syncwarp();
+                add = true;
+                if (++st == PL::kStages) st = 0, ph ^= 1;
+              }
+            }
+          if (lead) mma_commit(accf + 8 * buf);
+          __syncwarp();
+          if (++buf == PL::kBufs) buf = 0, bph ^= 1;
         }
       }
     }
@@ -624,9 +650,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
       if (lane == 0) bar_arrive_cluster(in_leader(acce + 8 * buf));
       if (++buf == PL::kBufs) buf = 0, bph ^= 1;
     };
+    Walk walk;
     for (int t = pair; t < p.tiles; t += pairs) {
-      const Tile ti = tile_of(p, t);
-      const Job& j = p.job[ti.job];
+      walk.seek(p, t);
+      const Tile ti = walk.tile(t);
+      const Job& j = p.job[walk.job];
       const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
       const long long m = m0 + row;
       const bool live = m < j.M;
@@ -635,7 +663,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
         constexpr int Q = EPI == kEpiOut ? 1 : EPI == kEpiHidden ? 2 : 3;
         constexpr int W = PL::kCols / 2;
         float sum[Q][W];
-        const int pieces = pieces_of<PL::kPiece>(p, j, ti.split);
+        int lo, hi;
+        walk.range(ti.split, lo, hi);
+        const int pieces = pieces_of<PL::kPiece>(lo, hi);
         bool yes = true;
         for (int pc = 0; pc < pieces; ++pc) {
           if (!(yes = arrived())) break;
@@ -677,30 +707,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
           with_act(p.act, [&](auto kind) {
             constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-            for (int i0 = 0; i0 < W; i0 += 8) {
-              uint32_t w[PL::kOuts][3][4];
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const float g[2] = {sum[0][i0 + i], sum[0][i0 + i + 1]}, u[2] = {sum[1][i0 + i], sum[1][i0 + i + 1]};
-                float r[3][2];
-                if constexpr (EPI == kEpiGrad) {
-                  const float d[2] = {sum[2][i0 + i], sum[2][i0 + i + 1]};
-                  hidden_grads2<true, ACT>(g, u, d, r[0], r[1], r[2]);
-                } else {
-                  hidden2<true, ACT>(g, u, r[0]);
-                }
-#pragma unroll
-                for (int q = 0; q < PL::kOuts; ++q) split3x2(r[q][0], r[q][1], w[q][0][i / 2], w[q][1][i / 2], w[q][2][i / 2]);
+            for (int i = 0; i < W; i += 2) {      // the hidden values take the place of the sums
+              const float g[2] = {sum[0][i], sum[0][i + 1]}, u[2] = {sum[1][i], sum[1][i + 1]};
+              float r[3][2];
+              if constexpr (EPI == kEpiGrad) {
+                const float d[2] = {sum[2][i], sum[2][i + 1]};
+                hidden_grads2<true, ACT>(g, u, d, r[0], r[1], r[2]);
+              } else {
+                hidden2<true, ACT>(g, u, r[0]);
               }
-              if (live && n0 + i0 < j.N)
 #pragma unroll
-                for (int q = 0; q < PL::kOuts; ++q)
-#pragma unroll
-                  for (int k = 0; k < 3; ++k)
-                    *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
-                        make_uint4(w[q][k][0], w[q][k][1], w[q][k][2], w[q][k][3]);
+              for (int q = 0; q < PL::kOuts; ++q) sum[q][i] = r[q][0], sum[q][i + 1] = r[q][1];
             }
           });
+#pragma unroll
+          for (int q = 0; q < PL::kOuts; ++q)
+#pragma unroll
+            for (int i0 = 0; i0 < W; i0 += 8) {
+              uint32_t w[3][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                split3x2(sum[q][i0 + 2 * i], sum[q][i0 + 2 * i + 1], w[0][i], w[1][i], w[2][i]);
+              if (live && n0 + i0 < j.N)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                  *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
+                      make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+            }
         }
       } else {
         if (!arrived()) break;

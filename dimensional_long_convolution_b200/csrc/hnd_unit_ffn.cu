@@ -279,25 +279,25 @@ struct Ffn {
   // activations as the rows of a product (m = positions): the position axis
   // is contiguous, except token-major, where the channels are
   int positions(Launch& n, const Mat& m) const { return l.token ? n.km(m) : n.mn(m); }
-  Seg data_seg(int ma, int mb, bool a_mn, bool b_mn, int ncols, int acc, int clear, long long depth) const {
-    return Seg{ma,  mb,    mb, a_mn, b_mn, l.batches > 1, 0, ncols, ncols, ncols / 2,
-               acc, clear, static_cast<int>(cdiv(depth, kBK))};
+  Seg data_seg(int ma, int mb, bool a_mn, bool b_mn, int ncols, int acc, int clear) const {
+    return Seg{ma, mb, mb, a_mn, b_mn, l.batches > 1, 0, ncols, ncols, ncols / 2, acc, clear};
   }
   // G and U of `cols` hidden channels side by side: the first CTA brings Wg, the second Wu
   Seg gates_seg(Launch& n, int cols) const {
-    Seg s = data_seg(positions(n, x), n.km(wg, cols), !l.token, false, 2 * cols, 0, 1, a.C);
+    Seg s = data_seg(positions(n, x), n.km(wg, cols), !l.token, false, 2 * cols, 0, 1);
     s.b1 = n.km(wu, cols);
     s.nstep = cols;
     s.noff = 0;
     return s;
   }
-  Job data_job(int nseg, long long N, int per_tile) const {
+  Job data_job(int nseg, long long N, int per_tile, long long depth) const {
     Job j{};
     j.nseg = nseg;
     j.batches = static_cast<int>(l.batches);
     j.mt = static_cast<int>(cdiv(l.Lx, 256));
     j.nt = static_cast<int>(cdiv(N, per_tile));
     j.splits = j.kbatches = 1;
+    j.kblocks = j.kper = static_cast<int>(cdiv(depth, kBK));
     j.M = l.Lx;
     j.N = N;
     return j;
@@ -331,11 +331,11 @@ struct Ffn {
     Launch h = start();
     h.p.seg[0] = gates_seg(h, hn);
     hidden_out(h, 1);
-    h.job(data_job(1, a.F, hn));
+    h.job(data_job(1, a.F, hn, a.C));
     if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
     Launch y = start();
-    y.p.seg[0] = data_seg(y.km(hid[0]), y.km(wd, on / 2), false, false, on, 0, 1, a.F);
-    Job j = data_job(1, a.C, on);
+    y.p.seg[0] = data_seg(y.km(hid[0]), y.km(wd, on / 2), false, false, on, 0, 1);
+    Job j = data_job(1, a.C, on, a.F);
     activation_out(y, j, a.y);
     y.job(j);
     return run<kEpiOut, F32>(y, a.stream);
@@ -349,16 +349,16 @@ struct Ffn {
     // H, dG, dU
     Launch h = start();
         h.p.seg[0] = gates_seg(h, gn);
-    h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, PG::kGradCols, 2 * gn, 1, a.C);
+    h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, PG::kGradCols, 2 * gn, 1);
     h.p.seg[1].nstep = gn;
     hidden_out(h, 3);
-    h.job(data_job(2, a.F, gn));
+    h.job(data_job(2, a.F, gn, a.C));
     if ((e = run<kEpiGrad, F32>(h, a.stream)) != cudaSuccess) return e;
     // dX
     Launch d = start();
-    d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1, a.F);
-    d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0, a.F);
-    Job j = data_job(2, a.C, on);
+    d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1);
+    d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0);
+    Job j = data_job(2, a.C, on, a.F);
     activation_out(d, j, a.dx);
     d.job(j);
     if ((e = run<kEpiOut, F32>(d, a.stream)) != cudaSuccess) return e;
@@ -369,7 +369,7 @@ struct Ffn {
     const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, on / 2);
     const int mh = w.mn(hid[0]), mdg = w.mn(hid[1]), mdu = w.mn(hid[2]);
     auto seg = [&](int ma, int mb, int a_mn, int b_mn) {
-      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 1, stages};
+      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 1};
     };
     w.p.seg[0] = seg(mx, mdg, l.token, 1);
     w.p.seg[1] = seg(mx, mdu, l.token, 1);
@@ -386,7 +386,9 @@ struct Ffn {
       q.nt = static_cast<int>(cdiv(q.N, on));
       q.batches = 1;
       q.kbatches = static_cast<int>(l.batches);
+      q.kblocks = stages;
       q.splits = l.splits;
+      q.kper = static_cast<int>(cdiv(l.batches * stages, l.splits));
       q.rs = q.M;
       q.bs = l.w_plane;
       if (l.splits > 1) {

@@ -42,7 +42,7 @@ struct JoinArgs {
 
 cudaError_t launch_join_forward(const JoinArgs& a);
 cudaError_t launch_join_backward(const JoinArgs& a);
-size_t join_workspace(long long B, long long C, long long L);
+size_t join_workspace(long long B, long long C, long long L, int bf16);
 
 cudaError_t launch_dropout(long long count, int bf16, const DropStage& d, const void* x, void* y, cudaStream_t st);
 

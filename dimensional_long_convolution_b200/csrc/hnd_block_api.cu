@@ -112,7 +112,7 @@ hyena_nd_status check_join(const hyena_nd_block_shape* s, const hyena_nd_join* j
   return HYENA_ND_OK;
 }
 
-size_t join_ws(const hyena_nd_block_shape* s) { return hnd::join_workspace(s->B, s->C, s->L); }
+size_t join_ws(const hyena_nd_block_shape* s) { return hnd::join_workspace(s->B, s->C, s->L, s->io_dtype == HYENA_ND_BF16); }
 
 hyena_nd_status join_backward(const hyena_nd_block_shape* s, hnd::JoinArgs& a, void* ws, size_t ws_bytes) {
   const size_t act = act_bytes(s), C4 = 4 * static_cast<size_t>(s->C), BC4 = C4 * static_cast<size_t>(s->B);

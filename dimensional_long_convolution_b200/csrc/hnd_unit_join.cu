@@ -1,23 +1,14 @@
 // The residual join with the norms on both sides of it, forward and backward.
-#include "hnd_block.h"
-#include "hnd_io.cuh"
-#include "hnd_philox.cuh"
+#include "hnd_join.cuh"
 
 namespace hnd {
 
+// ----------------------------------------- any number of channels, any length
+// For more channels than a block of hnd_join.cuh holds in registers (4096
+// forward, 2048 in the gradients of grids): a block takes 32 positions and
+// reads their channels again for each of its sweeps, from L2 mostly.
 constexpr int kJoinLanes = 32;   // positions of a block
 constexpr int kJoinRows = 8;     // channel rows of a block
-
-// Everything a kernel needs of a join, by value.
-struct JoinDev {
-  long long B, C, L, T;
-  int post, pre;
-  float eps1, eps2;
-  const float *w1, *b1, *w2, *b2, *gate, *scale;
-  unsigned border;
-  float factor;
-  const int64_t* rng;
-};
 
 // One position's view of the join: values at channel c.
 template <class TT>
@@ -108,7 +99,7 @@ __device__ __forceinline__ void pos_stats(Pos<TT>& p, bool live, float (*buf)[kJ
 
 template <class TT>
 __global__ void __launch_bounds__(kJoinLanes* kJoinRows)
-    k_join_fwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, TT* __restrict__ h, TT* __restrict__ n) {
+    k_join_any_fwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, TT* __restrict__ h, TT* __restrict__ n) {
   __shared__ float buf[kJoinRows][kJoinLanes];
   const long long t = blockIdx.x * static_cast<long long>(kJoinLanes) + threadIdx.x;
   const bool live = t < j.T;
@@ -137,7 +128,7 @@ __device__ __forceinline__ float whole_grad(const Pos<TT>& p, const TT* dh, cons
 
 template <class TT>
 __global__ void __launch_bounds__(kJoinLanes* kJoinRows)
-    k_join_bwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
+    k_join_any_bwd(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
                const TT* __restrict__ dn, TT* __restrict__ dx, TT* __restrict__ dy, JoinStat* __restrict__ stats) {
   __shared__ float buf[kJoinRows][kJoinLanes];
   const long long t = blockIdx.x * static_cast<long long>(kJoinLanes) + threadIdx.x;
@@ -183,7 +174,7 @@ __global__ void __launch_bounds__(kJoinLanes* kJoinRows)
 // Per (b, c): sums over the positions of dht m yhat, dht m, dn hhat, dn.
 template <class TT>
 __global__ void __launch_bounds__(256)
-    k_join_param(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
+    k_join_any_param(JoinDev j, const TT* __restrict__ x, const TT* __restrict__ y, const TT* __restrict__ dh,
                  const TT* __restrict__ dn, const JoinStat* __restrict__ stats, float4* __restrict__ part) {
   const long long bc = blockIdx.x, b = bc / j.C, c = bc % j.C;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -219,68 +210,168 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) *HND_G(part + bc) = buf[0];
 }
 
-struct JoinGradsDev {
-  float *w1, *b1, *gate, *scale, *w2, *b2;
-};
-
-__global__ void __launch_bounds__(256) k_join_grads(JoinDev j, const float4* __restrict__ part, JoinGradsDev g) {
-  const long long c = blockIdx.x * 256LL + threadIdx.x;
-  if (c >= j.C) return;
-  const float w1 = j.w1 ? ld1(j.w1 + c) : 1.f, b1 = j.b1 ? ld1(j.b1 + c) : 0.f;
-  const float sc = j.scale ? ld1(j.scale + c) : 1.f;
-  float dw1 = 0.f, db1 = 0.f, ds = 0.f, dw2 = 0.f, db2 = 0.f;
-  for (long long b = 0; b < j.B; ++b) {
-    const float4 s = *HND_G(part + b * j.C + c);
-    const float gt = j.gate ? ld1(j.gate + b * j.C + c) : 1.f;
-    const float z = w1 * s.x + b1 * s.y;
-    if (g.gate) st1(g.gate + b * j.C + c, sc * z);
-    dw1 += sc * gt * s.x;
-    db1 += sc * gt * s.y;
-    ds += gt * z;
-    dw2 += s.z;
-    db2 += s.w;
-  }
-  if (g.w1) st1(g.w1 + c, dw1);
-  if (g.b1) st1(g.b1 + c, db1);
-  if (g.scale) st1(g.scale + c, ds);
-  if (g.w2) st1(g.w2 + c, dw2);
-  if (g.b2) st1(g.b2 + c, db2);
-}
-
 static JoinDev device_view(const JoinArgs& a) {
   return {a.B,      a.C,      a.L,    a.B * a.L, a.post.kind, a.pre.kind,    a.post.eps,    a.pre.eps, a.post.w,
           a.post.b, a.pre.w,  a.pre.b, a.gate,    a.scale,     a.drop.border, a.drop.factor, a.drop.rng};
 }
 
-template <class TT>
-static cudaError_t forward(const JoinArgs& a) {
-  const JoinDev j = device_view(a);
-  const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
-  k_join_fwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(
-      j, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h), static_cast<TT*>(a.n));
-  return cudaGetLastError();
+// ------------------------------------------------------------------ launches
+static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+static int pow2_up(long long v) {
+  int p = 1;
+  while (p < v) p *= 2;
+  return p;
+}
+
+// How a call runs; a function of the shape alone.
+struct JoinPlan {
+  bool fast = false;       // hnd_join.cuh; else the kernels above
+  int V = 1, K = 1;        // values of a vector, vectors of a thread
+  int lanes = 0;           // grid: neighbouring vectors of positions; token: threads of a position
+  int threads = 0;
+  long long blocks = 0;
+  int chunks = 1;          // gradients on grids: blocks of a sample
+  long long rows = 0;      // gradients: rows of partial sums
+};
+
+constexpr long long kJoinParts = 592;     // blocks of a gradient call: four an SM
+
+// Grid layout: the widest row of positions whose channels fit a block.
+static bool grid_plan(JoinPlan& p, long long C, long long units, int widest) {
+  const long long rows = cdiv(C, p.K);
+  int w = widest;
+  while (w > 1 && w / 2 >= units) w /= 2;
+  // 256 threads, so that two blocks share an SM, unless that makes rows shorter than four vectors (32 for V = 1)
+  const int least = widest / 2 < w ? widest / 2 : w;
+  for (int cap : {256, kJoinMaxThreads})
+    for (int v = w; v >= (cap == 256 ? least : 1); v /= 2)
+      if (cdiv(v * rows, 32) * 32 <= cap) {
+        p.lanes = v;
+        p.threads = static_cast<int>(cdiv(v * rows, 32) * 32);
+        return true;
+      }
+  return false;
+}
+
+static JoinPlan join_plan(long long B, long long C, long long L, int bf16, bool backward) {
+  JoinPlan p;
+  const int wide = bf16 ? 8 : 4;
+  const bool token = L == 1;
+  p.V = (token ? C : L) % wide == 0 ? wide : 1;
+  if (token) {
+    const long long vectors = C / p.V;
+    // few positions: a thread for each vector, for the shortest way through; else several, for fewer threads a row
+    const int most = backward ? (p.V == 1 ? 8 : 16 / p.V) : p.V == 1 ? 16 : 32 / p.V;
+    p.K = B <= 296 && vectors <= kJoinMaxThreads ? 1 : most;
+    const long long t = cdiv(cdiv(vectors, p.K), 32) * 32;
+    if (t > kJoinMaxThreads) return p;
+    p.lanes = static_cast<int>(t);
+    const long long groups = B > 296 && t < 256 ? 256 / t : 1;
+    p.threads = static_cast<int>(t * groups);
+    const long long tiles = cdiv(B, groups);
+    p.blocks = tiles;
+    if (backward) {
+      const long long most_blocks = kJoinParts / groups;
+      p.blocks = tiles < most_blocks ? tiles : most_blocks;
+      p.rows = p.blocks * groups;
+    }
+  } else {
+    const long long per = L / p.V, units = backward ? per : per * B;
+    if (backward)
+      p.K = p.V == 1 ? 8 : 4;
+    else
+      p.K = p.V == 1 ? (C <= 64 ? 8 : 32) : C <= 64 ? 2 : 32 / wide;
+    if (!grid_plan(p, C, units, p.V == 1 ? 32 : 8)) return p;
+    if (backward) {
+      const long long tiles = cdiv(per, p.lanes), want = cdiv(kJoinParts, B);
+      p.chunks = static_cast<int>(tiles < want ? tiles : want);
+      p.blocks = p.rows = B * p.chunks;
+    } else {
+      p.blocks = cdiv(units, p.lanes);
+    }
+  }
+  p.fast = p.blocks < 1LL << 31;
+  return p;
+}
+
+static size_t plan_smem(const JoinPlan& p, bool token) {
+  const int sets = token ? 1 : p.lanes, positions = token ? 1 : p.V;
+  return sizeof(float) * 2 * (p.threads / 32) * sets * 2 * positions;
 }
 
 static size_t stats_bytes(long long T) { return (static_cast<size_t>(T) * sizeof(JoinStat) + 255) / 256 * 256; }
 
-size_t join_workspace(long long B, long long C, long long L) {
+size_t join_workspace(long long B, long long C, long long L, int bf16) {
+  const JoinPlan p = join_plan(B, C, L, bf16, true);
+  if (p.fast) return static_cast<size_t>(p.rows) * C * sizeof(float4);
   return stats_bytes(B * L) + static_cast<size_t>(B * C) * sizeof(float4);
+}
+
+template <class TT, int V, int K, bool TOK>
+static cudaError_t forward_as(const JoinArgs& a, const JoinPlan& p) {
+  k_join_fwd<TT, V, K, TOK><<<static_cast<unsigned>(p.blocks), p.threads, plan_smem(p, TOK), a.stream>>>(
+      device_view(a), p.lanes, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h),
+      static_cast<TT*>(a.n));
+  return cudaGetLastError();
+}
+
+template <class TT>
+static cudaError_t forward(const JoinArgs& a) {
+  constexpr int W = sizeof(TT) == 2 ? 8 : 4;
+  const JoinPlan p = join_plan(a.B, a.C, a.L, a.bf16, false);
+  if (!p.fast) {
+    const JoinDev j = device_view(a);
+    const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
+    k_join_any_fwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(
+        j, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h), static_cast<TT*>(a.n));
+    return cudaGetLastError();
+  }
+  if (a.L == 1) {
+    if (p.V == 1) return p.K == 1 ? forward_as<TT, 1, 1, true>(a, p) : forward_as<TT, 1, 16, true>(a, p);
+    return p.K == 1 ? forward_as<TT, W, 1, true>(a, p) : forward_as<TT, W, 32 / W, true>(a, p);
+  }
+  if (p.V == 1) return p.K == 8 ? forward_as<TT, 1, 8, false>(a, p) : forward_as<TT, 1, 32, false>(a, p);
+  return p.K == 2 ? forward_as<TT, W, 2, false>(a, p) : forward_as<TT, W, 32 / W, false>(a, p);
+}
+
+template <class TT, int V, int K, bool TOK>
+static cudaError_t backward_as(const JoinArgs& a, const JoinPlan& p) {
+  const JoinDev j = device_view(a);
+  const bool params = a.dpost_w || a.dpost_b || a.dscale || a.dpre_w || a.dpre_b || (a.dgate && !TOK);
+  float4* part = static_cast<float4*>(a.ws);
+  k_join_bwd<TT, V, K, TOK><<<static_cast<unsigned>(p.blocks), p.threads, plan_smem(p, TOK), a.stream>>>(
+      j, p.lanes, p.chunks, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<const TT*>(a.dh),
+      static_cast<const TT*>(a.dn), static_cast<TT*>(a.dx), static_cast<TT*>(a.dy), a.dgate, params ? part : nullptr);
+  if (params)
+    k_join_grads<<<static_cast<unsigned>(cdiv(a.C, 32) * (a.dgate && !TOK ? 1 + a.B : 1)), dim3(32, 32), 0,
+                   a.stream>>>(j, part, p.rows, TOK ? 0 : p.chunks,
+                               JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
+  return cudaGetLastError();
 }
 
 template <class TT>
 static cudaError_t backward(const JoinArgs& a) {
+  constexpr int W = sizeof(TT) == 2 ? 8 : 4;
+  const JoinPlan p = join_plan(a.B, a.C, a.L, a.bf16, true);
+  if (p.fast) {
+    if (a.L == 1) {
+      if (p.V == 1) return p.K == 1 ? backward_as<TT, 1, 1, true>(a, p) : backward_as<TT, 1, 8, true>(a, p);
+      return p.K == 1 ? backward_as<TT, W, 1, true>(a, p) : backward_as<TT, W, 16 / W, true>(a, p);
+    }
+    return p.V == 1 ? backward_as<TT, 1, 8, false>(a, p) : backward_as<TT, W, 4, false>(a, p);
+  }
   const JoinDev j = device_view(a);
   const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
   JoinStat* stats = static_cast<JoinStat*>(a.ws);
   float4* part = reinterpret_cast<float4*>(static_cast<char*>(a.ws) + stats_bytes(j.T));
   const TT *x = static_cast<const TT*>(a.x), *y = static_cast<const TT*>(a.y), *dh = static_cast<const TT*>(a.dh),
            *dn = static_cast<const TT*>(a.dn);
-  k_join_bwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(j, x, y, dh, dn, static_cast<TT*>(a.dx),
-                                                                      static_cast<TT*>(a.dy), stats);
+  k_join_any_bwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(j, x, y, dh, dn, static_cast<TT*>(a.dx),
+                                                                          static_cast<TT*>(a.dy), stats);
   if (a.dpost_w || a.dpost_b || a.dgate || a.dscale || a.dpre_w || a.dpre_b) {
-    k_join_param<TT><<<static_cast<unsigned>(j.B * j.C), 256, 0, a.stream>>>(j, x, y, dh, dn, stats, part);
-    k_join_grads<<<static_cast<unsigned>((j.C + 255) / 256), 256, 0, a.stream>>>(
-        j, part, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
+    k_join_any_param<TT><<<static_cast<unsigned>(j.B * j.C), 256, 0, a.stream>>>(j, x, y, dh, dn, stats, part);
+    k_join_grads<<<static_cast<unsigned>(cdiv(a.C, 32) * (a.dgate ? 1 + a.B : 1)), dim3(32, 32), 0, a.stream>>>(
+        j, part, j.B, 1, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
   }
   return cudaGetLastError();
 }

@@ -34,6 +34,12 @@ struct JoinDev {
   const int64_t* rng;
 };
 
+// The aligned-grid kernels of hnd_join_grid.cuh: K channels of a thread, w
+// lanes of positions, and (gradients) `chunks` blocks a sample.
+cudaError_t launch_join_grid_fwd(const JoinArgs& a, const JoinDev& j, int w, int K, unsigned blocks);
+cudaError_t launch_join_grid_bwd(const JoinArgs& a, const JoinDev& j, int w, int K, int chunks, unsigned blocks,
+                                 float4* part);
+
 // V neighbouring values as they are stored.
 template <class TT, int V>
 struct alignas(sizeof(TT) * V) Raw {
@@ -130,14 +136,15 @@ struct Tile {
       for (int i = 0; i < P; ++i)
         for (int o = 16; o >= first; o >>= 1) s[n][i] += __shfl_xor_sync(0xFFFFFFFFu, s[n][i], o);
     if (TOK && lanes == 32) return;
-    // what a warp writes: token: one set; grid: one of each of its (at most 32) lanes
+    // what a warp writes: token: one set; grid: one of each of its (at most
+    // 32) lanes, lanes side by side
     const int l = TOK ? 0 : lane, sets = TOK ? 1 : lanes;
-    float* out = buf + (flip * warps + warp) * sets * (2 * P);
+    float* out = buf + (flip * warps + warp) * sets * (2 * P) + l;
     if ((threadIdx.x & 31) < sets)
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < P; ++i) out[l * (2 * P) + n * P + i] = s[n][i];
+        for (int i = 0; i < P; ++i) out[(n * P + i) * sets] = s[n][i];
     __syncthreads();
     const int from = TOK ? warp / (lanes / 32) * (lanes / 32) : 0, to = TOK ? from + lanes / 32 : warps;
 #pragma unroll
@@ -145,11 +152,11 @@ struct Tile {
 #pragma unroll
       for (int i = 0; i < P; ++i) s[n][i] = 0.f;
     for (int w = from; w < to; ++w) {
-      const float* in = buf + ((flip * warps + w) * sets + l) * (2 * P);
+      const float* in = buf + (flip * warps + w) * sets * (2 * P) + l;
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < P; ++i) s[n][i] += in[n * P + i];
+        for (int i = 0; i < P; ++i) s[n][i] += in[(n * P + i) * sets];
     }
     flip ^= 1;      // the next sums go to the other half: no second barrier
   }
@@ -442,55 +449,6 @@ __global__ void __launch_bounds__(kJoinMaxThreads)
         *HND_G(part + row * j.C + t.chan(k) + a) = s;
       }
     }
-}
-
-struct JoinGradsDev {
-  float *w1, *b1, *gate, *scale, *w2, *b2;
-};
-
-// The parameters' gradients from the blocks' sums, `per` rows a sample (0:
-// already weighted with the gate).  The first ceil(C / 32) blocks sum over
-// all rows, the next over those of sample 0 for its gate, and so on.
-__global__ void __launch_bounds__(1024)
-    k_join_grads(const JoinDev j, const float4* __restrict__ part, long long rows, long long per, JoinGradsDev g) {
-  __shared__ float buf[4][32][33];
-  const unsigned wide = static_cast<unsigned>((j.C + 31) / 32);
-  const long long c = blockIdx.x % wide * 32LL + threadIdx.x, gate_of = static_cast<long long>(blockIdx.x / wide) - 1;
-  const bool live = c < j.C;
-  const long long lo = gate_of < 0 ? 0 : gate_of * per, hi = gate_of < 0 ? rows : lo + per;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live)
-    for (long long r = lo + threadIdx.y; r < hi; r += 32) {
-      const float4 v = *HND_G(part + r * j.C + c);
-      const float gt = gate_of < 0 && per && j.gate ? __ldg(HND_G(j.gate + r / per * j.C + c)) : 1.f;
-      s.x += gt * v.x, s.y += gt * v.y, s.z += v.z, s.w += v.w;
-    }
-  buf[0][threadIdx.y][threadIdx.x] = s.x;
-  buf[1][threadIdx.y][threadIdx.x] = s.y;
-  buf[2][threadIdx.y][threadIdx.x] = s.z;
-  buf[3][threadIdx.y][threadIdx.x] = s.w;
-  __syncthreads();
-  // warp q of the first four adds up value q
-  if (threadIdx.y < 4) {
-    float v = 0.f;
-    for (int r = 0; r < 32; ++r) v += buf[threadIdx.y][r][threadIdx.x];
-    __syncwarp();
-    buf[threadIdx.y][0][threadIdx.x] = v;
-  }
-  __syncthreads();
-  if (threadIdx.y || !live) return;
-  const float q = buf[0][0][threadIdx.x], r = buf[1][0][threadIdx.x];
-  const float w1 = j.w1 ? ld1(j.w1 + c) : 1.f, b1 = j.b1 ? ld1(j.b1 + c) : 0.f, sc = j.scale ? ld1(j.scale + c) : 1.f;
-  const float z = w1 * q + b1 * r;
-  if (gate_of >= 0) {
-    st1(g.gate + gate_of * j.C + c, sc * z);
-    return;
-  }
-  if (g.w1) st1(g.w1 + c, sc * q);
-  if (g.b1) st1(g.b1 + c, sc * r);
-  if (g.scale) st1(g.scale + c, z);
-  if (g.w2) st1(g.w2 + c, buf[2][0][threadIdx.x]);
-  if (g.b2) st1(g.b2 + c, buf[3][0][threadIdx.x]);
 }
 
 }  // namespace hnd

@@ -210,6 +210,56 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) *HND_G(part + bc) = buf[0];
 }
 
+// ------------------------------------------------- gradients of parameters
+struct JoinGradsDev {
+  float *w1, *b1, *gate, *scale, *w2, *b2;
+};
+
+// The parameters' gradients from the blocks' sums, `per` rows a sample (0:
+// already weighted with the gate).  The first ceil(C / 32) blocks sum over
+// all rows, the next over those of sample 0 for its gate, and so on.
+__global__ void __launch_bounds__(1024)
+    k_join_grads(const JoinDev j, const float4* __restrict__ part, long long rows, long long per, JoinGradsDev g) {
+  __shared__ float buf[4][32][33];
+  const unsigned wide = static_cast<unsigned>((j.C + 31) / 32);
+  const long long c = blockIdx.x % wide * 32LL + threadIdx.x, gate_of = static_cast<long long>(blockIdx.x / wide) - 1;
+  const bool live = c < j.C;
+  const long long lo = gate_of < 0 ? 0 : gate_of * per, hi = gate_of < 0 ? rows : lo + per;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live)
+    for (long long r = lo + threadIdx.y; r < hi; r += 32) {
+      const float4 v = *HND_G(part + r * j.C + c);
+      const float gt = gate_of < 0 && per && j.gate ? __ldg(HND_G(j.gate + r / per * j.C + c)) : 1.f;
+      s.x += gt * v.x, s.y += gt * v.y, s.z += v.z, s.w += v.w;
+    }
+  buf[0][threadIdx.y][threadIdx.x] = s.x;
+  buf[1][threadIdx.y][threadIdx.x] = s.y;
+  buf[2][threadIdx.y][threadIdx.x] = s.z;
+  buf[3][threadIdx.y][threadIdx.x] = s.w;
+  __syncthreads();
+  // warp q of the first four adds up value q
+  if (threadIdx.y < 4) {
+    float v = 0.f;
+    for (int r = 0; r < 32; ++r) v += buf[threadIdx.y][r][threadIdx.x];
+    __syncwarp();
+    buf[threadIdx.y][0][threadIdx.x] = v;
+  }
+  __syncthreads();
+  if (threadIdx.y || !live) return;
+  const float q = buf[0][0][threadIdx.x], r = buf[1][0][threadIdx.x];
+  const float w1 = j.w1 ? ld1(j.w1 + c) : 1.f, b1 = j.b1 ? ld1(j.b1 + c) : 0.f, sc = j.scale ? ld1(j.scale + c) : 1.f;
+  const float z = w1 * q + b1 * r;
+  if (gate_of >= 0) {
+    st1(g.gate + gate_of * j.C + c, sc * z);
+    return;
+  }
+  if (g.w1) st1(g.w1 + c, sc * q);
+  if (g.b1) st1(g.b1 + c, sc * r);
+  if (g.scale) st1(g.scale + c, z);
+  if (g.w2) st1(g.w2 + c, buf[2][0][threadIdx.x]);
+  if (g.b2) st1(g.b2 + c, buf[3][0][threadIdx.x]);
+}
+
 static JoinDev device_view(const JoinArgs& a) {
   return {a.B,      a.C,      a.L,    a.B * a.L, a.post.kind, a.pre.kind,    a.post.eps,    a.pre.eps, a.post.w,
           a.post.b, a.pre.w,  a.pre.b, a.gate,    a.scale,     a.drop.border, a.drop.factor, a.drop.rng};
@@ -226,6 +276,7 @@ static int pow2_up(long long v) {
 // How a call runs; a function of the shape alone.
 struct JoinPlan {
   bool fast = false;       // hnd_join.cuh; else the kernels above
+  bool ahead = false;      // hnd_join_grid.cuh
   int V = 1, K = 1;        // values of a vector, vectors of a thread
   int lanes = 0;           // grid: neighbouring vectors of positions; token: threads of a position
   int threads = 0;
@@ -253,8 +304,33 @@ static bool grid_plan(JoinPlan& p, long long C, long long units, int widest) {
   return false;
 }
 
+// Aligned grids of up to 512 channels (bf16 forward; 1024 and 512 of fp32):
+// as many lanes of positions as leave threads for the channels.
+static bool ahead_plan(JoinPlan& p, long long B, long long C, long long L, int bf16, bool backward) {
+  const int V = bf16 ? 8 : 4, most = backward || bf16 ? 4 : 8;
+  if (L == 1 || L % V) return false;
+  const long long per = L / V, units = backward ? per : per * B;
+  p.K = C <= 32 ? 1 : most;
+  int w = 32;
+  while (w > 2 && (256 / w * p.K < C || w / 2 >= units)) w /= 2;
+  if (256 / w * p.K < C) return false;
+  p.V = V;
+  p.lanes = w;
+  const long long tiles = cdiv(units, w);
+  if (backward) {
+    const long long want = B < kJoinParts / 2 ? kJoinParts / 2 / B : 1;      // two blocks an SM, in one wave
+    p.chunks = static_cast<int>(tiles < want ? tiles : want);
+    p.blocks = p.rows = B * p.chunks;
+  } else {
+    p.blocks = tiles < 444 ? tiles : 444;                                    // three an SM
+  }
+  p.fast = p.ahead = true;
+  return true;
+}
+
 static JoinPlan join_plan(long long B, long long C, long long L, int bf16, bool backward) {
   JoinPlan p;
+  if (ahead_plan(p, B, C, L, bf16, backward)) return p;
   const int wide = bf16 ? 8 : 4;
   const bool token = L == 1;
   p.V = (token ? C : L) % wide == 0 ? wide : 1;
@@ -280,7 +356,7 @@ static JoinPlan join_plan(long long B, long long C, long long L, int bf16, bool 
     if (backward)
       p.K = p.V == 1 ? 8 : 4;
     else
-      p.K = p.V == 1 ? (C <= 64 ? 8 : 32) : C <= 64 ? 2 : 32 / wide;
+      p.K = p.V == 1 ? (C <= 256 ? 8 : 32) : 32 / wide;
     if (!grid_plan(p, C, units, p.V == 1 ? 32 : 8)) return p;
     if (backward) {
       const long long tiles = cdiv(per, p.lanes), want = cdiv(kJoinParts, B);
@@ -326,26 +402,29 @@ static cudaError_t forward(const JoinArgs& a) {
         j, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h), static_cast<TT*>(a.n));
     return cudaGetLastError();
   }
+  if (p.ahead) return launch_join_grid_fwd(a, device_view(a), p.lanes, p.K, static_cast<unsigned>(p.blocks));
   if (a.L == 1) {
     if (p.V == 1) return p.K == 1 ? forward_as<TT, 1, 1, true>(a, p) : forward_as<TT, 1, 16, true>(a, p);
     return p.K == 1 ? forward_as<TT, W, 1, true>(a, p) : forward_as<TT, W, 32 / W, true>(a, p);
   }
   if (p.V == 1) return p.K == 8 ? forward_as<TT, 1, 8, false>(a, p) : forward_as<TT, 1, 32, false>(a, p);
-  return p.K == 2 ? forward_as<TT, W, 2, false>(a, p) : forward_as<TT, W, 32 / W, false>(a, p);
+  return forward_as<TT, W, 32 / W, false>(a, p);
+}
+
+// The parameters' gradients from `rows` rows of sums, `per` a sample.
+static cudaError_t grads(const JoinArgs& a, const float4* part, long long rows, long long per) {
+  const long long wide = cdiv(a.C, 32);
+  k_join_grads<<<static_cast<unsigned>(wide * (a.dgate && per ? 1 + a.B : 1)), dim3(32, 32), 0, a.stream>>>(
+      device_view(a), part, rows, per, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
+  return cudaGetLastError();
 }
 
 template <class TT, int V, int K, bool TOK>
-static cudaError_t backward_as(const JoinArgs& a, const JoinPlan& p) {
-  const JoinDev j = device_view(a);
-  const bool params = a.dpost_w || a.dpost_b || a.dscale || a.dpre_w || a.dpre_b || (a.dgate && !TOK);
-  float4* part = static_cast<float4*>(a.ws);
+static cudaError_t backward_as(const JoinArgs& a, const JoinPlan& p, float4* part) {
   k_join_bwd<TT, V, K, TOK><<<static_cast<unsigned>(p.blocks), p.threads, plan_smem(p, TOK), a.stream>>>(
-      j, p.lanes, p.chunks, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<const TT*>(a.dh),
-      static_cast<const TT*>(a.dn), static_cast<TT*>(a.dx), static_cast<TT*>(a.dy), a.dgate, params ? part : nullptr);
-  if (params)
-    k_join_grads<<<static_cast<unsigned>(cdiv(a.C, 32) * (a.dgate && !TOK ? 1 + a.B : 1)), dim3(32, 32), 0,
-                   a.stream>>>(j, part, p.rows, TOK ? 0 : p.chunks,
-                               JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
+      device_view(a), p.lanes, p.chunks, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y),
+      static_cast<const TT*>(a.dh), static_cast<const TT*>(a.dn), static_cast<TT*>(a.dx), static_cast<TT*>(a.dy),
+      a.dgate, part);
   return cudaGetLastError();
 }
 
@@ -353,12 +432,20 @@ template <class TT>
 static cudaError_t backward(const JoinArgs& a) {
   constexpr int W = sizeof(TT) == 2 ? 8 : 4;
   const JoinPlan p = join_plan(a.B, a.C, a.L, a.bf16, true);
+  const bool token = a.L == 1;
+  const bool params = a.dpost_w || a.dpost_b || a.dscale || a.dpre_w || a.dpre_b || (a.dgate && !(token && p.fast));
   if (p.fast) {
-    if (a.L == 1) {
-      if (p.V == 1) return p.K == 1 ? backward_as<TT, 1, 1, true>(a, p) : backward_as<TT, 1, 8, true>(a, p);
-      return p.K == 1 ? backward_as<TT, W, 1, true>(a, p) : backward_as<TT, W, 16 / W, true>(a, p);
-    }
-    return p.V == 1 ? backward_as<TT, 1, 8, false>(a, p) : backward_as<TT, W, 4, false>(a, p);
+    float4* part = params ? static_cast<float4*>(a.ws) : nullptr;
+    cudaError_t e;
+    if (p.ahead)
+      e = launch_join_grid_bwd(a, device_view(a), p.lanes, p.K, p.chunks, static_cast<unsigned>(p.blocks), part);
+    else if (token && p.V == 1)
+      e = p.K == 1 ? backward_as<TT, 1, 1, true>(a, p, part) : backward_as<TT, 1, 8, true>(a, p, part);
+    else if (token)
+      e = p.K == 1 ? backward_as<TT, W, 1, true>(a, p, part) : backward_as<TT, W, 16 / W, true>(a, p, part);
+    else
+      e = p.V == 1 ? backward_as<TT, 1, 8, false>(a, p, part) : backward_as<TT, W, 4, false>(a, p, part);
+    return e == cudaSuccess && params ? grads(a, part, p.rows, token ? 0 : p.chunks) : e;
   }
   const JoinDev j = device_view(a);
   const unsigned blocks = static_cast<unsigned>((j.T + kJoinLanes - 1) / kJoinLanes);
@@ -368,12 +455,10 @@ static cudaError_t backward(const JoinArgs& a) {
            *dn = static_cast<const TT*>(a.dn);
   k_join_any_bwd<TT><<<blocks, dim3(kJoinLanes, kJoinRows), 0, a.stream>>>(j, x, y, dh, dn, static_cast<TT*>(a.dx),
                                                                           static_cast<TT*>(a.dy), stats);
-  if (a.dpost_w || a.dpost_b || a.dgate || a.dscale || a.dpre_w || a.dpre_b) {
-    k_join_any_param<TT><<<static_cast<unsigned>(j.B * j.C), 256, 0, a.stream>>>(j, x, y, dh, dn, stats, part);
-    k_join_grads<<<static_cast<unsigned>(cdiv(a.C, 32) * (a.dgate ? 1 + a.B : 1)), dim3(32, 32), 0, a.stream>>>(
-        j, part, j.B, 1, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
-  }
-  return cudaGetLastError();
+  if (!params) return cudaGetLastError();
+  k_join_any_param<TT><<<static_cast<unsigned>(j.B * j.C), 256, 0, a.stream>>>(j, x, y, dh, dn, stats, part);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? grads(a, part, j.B, 1) : e;
 }
 
 cudaError_t launch_join_forward(const JoinArgs& a) {

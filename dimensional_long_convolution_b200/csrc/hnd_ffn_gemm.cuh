@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "hnd_bounds.cuh"
+#include "hnd_div.cuh"
 
 namespace hnd {
 namespace ffn {
@@ -66,32 +67,15 @@ enum OutKind {
   kOutTok = 3       // token-major: a lane's columns are adjacent
 };
 
-// Division by a number fixed at launch: n / d = (n mul) >> 32 for 0 <= n <
-// 2^31, with mul = ceil(2^(32 + s) / d) and a shift (Granlund and Montgomery,
-// "Division by invariant integers using multiplication", 1994).  The single
-// threads that issue copies and products find their tile with it: with plain
-// divisions that took longer than a short tile's products.
-struct Div {
-  uint32_t d, mul, shift;
-  __device__ __forceinline__ int quot(int n) const {
-    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
-  }
-};
-inline Div make_div(uint32_t d) {
-  uint32_t s = 0;
-  while ((1ull << s) < d) ++s;                 // 2^(s-1) < d <= 2^s
-  if (s == 0) return Div{1, 0, 0};
-  // mul < 2^32 as d > 2^(s-1); exact for n < 2^31
-  return Div{d, static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), s - 1};
-}
-
 // One product: tiles [batches][mt][nt][splits].
 struct Job {
   int seg0, nseg;
   int batches, mt, nt, splits;
   int kbatches, kblocks;     // the K loop: batches (of weight gradients), stages of each
   int kper;                  // stages of a split
-  Div per, group8, mdiv;     // tiles of a split, of eight m tiles; mt
+  // tiles of a split, tiles of eight m tiles, mt: with plain divisions the
+  // issuing warps took longer to find a short tile than its products do
+  Div per, group8, mdiv;
   long long M, N;            // extents of D
   int kind, map;             // how D leaves, and the map of kOutTma
   void* ptr;                 // D otherwise: element (m, n) of split s at

@@ -15,6 +15,7 @@
 // threads the channels, K apiece.
 #pragma once
 
+#include "hnd_div.cuh"
 #include "hnd_join.cuh"
 
 namespace hnd {
@@ -91,26 +92,37 @@ inline size_t smem_bytes(int tensors, int K, long long C, int w, int V) {
   return static_cast<size_t>(tensors) * K * kT * 16 + static_cast<size_t>(C) * 16 + sizeof(float) * (kWarps + 1) * 2 * w * V;
 }
 
+// Where a thread's vectors of a tile lie: its first element, its sample, and a
+// bit for each of its channels that is there.
+struct Spot {
+  long long at;
+  int b;
+  unsigned on;
+};
+
 template <class TT, int K>
 struct Grid {
   static constexpr int Q = Vec<TT>::Q, V = 2 * Q;
   const JoinDev& j;
-  const int w, lane, cg, rows;
-  const long long per;              // vectors of a row
+  const int w, lane, cg, rows, C;
+  unsigned chans = 0;               // bit k: channel k of the thread exists
+  long long own, step;              // of its first channel in a sample, and from one of its channels to the next
   uint4* slots;
   float4* coef;                     // of a channel: scale w1, scale b1, w2, b2
   float* part;                      // [kWarps][2 V w]
   float* total;                     // [2 V w]
-  long long base = 0, b = 0;
-  bool live = false;
 
   __device__ Grid(const JoinDev& jj, int lanes, int tensors, unsigned char* smem)
-      : j(jj), w(lanes), lane(threadIdx.x % lanes), cg(threadIdx.x / lanes), rows(kT / lanes), per(jj.L / V) {
-    slots = reinterpret_cast<uint4*>(smem);
-    coef = reinterpret_cast<float4*>(slots + tensors * K * kT);
-    part = reinterpret_cast<float*>(coef + j.C);
+      : j(jj), w(lanes), lane(threadIdx.x % lanes), cg(threadIdx.x / lanes), rows(kT / lanes), C(static_cast<int>(jj.C)) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) chans |= static_cast<unsigned>(chan(k) < C) << k;
+    own = cg * j.L;
+    step = rows * j.L;
+    slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    coef = reinterpret_cast<float4*>(reinterpret_cast<uint4*>(smem) + tensors * K * kT);
+    part = reinterpret_cast<float*>(coef + C);
     total = part + kWarps * 2 * V * w;
-    for (int c = threadIdx.x; c < j.C; c += kT) {
+    for (int c = threadIdx.x; c < C; c += kT) {
       const float sc = j.scale ? __ldg(HND_G(j.scale + c)) : 1.f;
       *HND_S(coef + c) = make_float4(sc * (j.w1 ? __ldg(HND_G(j.w1 + c)) : 1.f), sc * (j.b1 ? __ldg(HND_G(j.b1 + c)) : 0.f),
                                      j.w2 ? __ldg(HND_G(j.w2 + c)) : 1.f, j.b2 ? __ldg(HND_G(j.b2 + c)) : 0.f);
@@ -118,25 +130,23 @@ struct Grid {
     __syncthreads();
   }
   __device__ int chan(int k) const { return cg + k * rows; }
-  __device__ bool has(int k) const { return live && chan(k) < j.C; }
-  __device__ long long at(int k) const { return base + chan(k) * j.L; }
-  __device__ uint4* slot(int tensor, int k) const { return slots + (tensor * K + k) * kT + threadIdx.x; }
-  __device__ uint4 raw(int tensor, int k) const { return *HND_S(slot(tensor, k)); }
-  __device__ float gate(int k) const { return j.gate ? __ldg(HND_G(j.gate + b * j.C + chan(k))) : 1.f; }
-  // Vector u of sample s.
-  __device__ void place(long long s, long long u, bool ok) {
-    live = ok;
-    b = ok ? s : 0;
-    base = b * j.C * j.L + (ok ? u * V : 0);
+  __device__ uint4 raw(int tensor, int k) const { return *HND_S(slots + (tensor * K + k) * kT); }
+  __device__ float gate(const Spot& s, int k) const {
+    return j.gate ? __ldg(HND_G(j.gate + static_cast<long long>(s.b) * C + chan(k))) : 1.f;
   }
-  __device__ void fetch(int tensor, const TT* p) const {
+  // Vector u of sample b.
+  __device__ Spot spot(int b, int u, bool live) const {
+    return Spot{live ? b * j.C * j.L + static_cast<long long>(u) * V + own : 0, live ? b : 0, live ? chans : 0u};
+  }
+  __device__ void fetch(const Spot& s, int tensor, const TT* p) const {
     if (!p) return;
+    const TT* from = p + s.at;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (has(k)) copy16(slot(tensor, k), p + at(k));
+    for (int k = 0; k < K; ++k, from += step)
+      if (s.on >> k & 1u) copy16(slots + (tensor * K + k) * kT, from);
   }
-  __device__ void store(TT* p, int k, const float2 (&f)[Q]) const {
-    __stcs(HND_G(reinterpret_cast<uint4*>(p + at(k))), Vec<TT>::put(f));
+  __device__ void store(const Spot& s, TT* p, int k, const float2 (&f)[Q]) const {
+    __stcs(HND_G(reinterpret_cast<uint4*>(p + (s.at + k * step))), Vec<TT>::put(f));
   }
 
   // Sums over the channels of N values at each of the thread's positions:
@@ -177,7 +187,7 @@ struct Grid {
   }
   // Mean (negative) and reciprocal deviation of f(k, q) at each position.
   template <class Fn>
-  __device__ void stats(int kind, float eps, float2 (&neg)[Q], float2 (&rho)[Q], Fn f) const {
+  __device__ void stats(const Spot& at, int kind, float eps, float2 (&neg)[Q], float2 (&rho)[Q], Fn f) const {
 #pragma unroll
     for (int q = 0; q < Q; ++q) neg[q] = both(0.f), rho[q] = both(1.f);
     if (!kind) return;
@@ -188,7 +198,7 @@ struct Grid {
       for (int q = 0; q < Q; ++q) s[0][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (has(k)) f(k, [&](int q, float2 v) { s[0][q] = add(s[0][q], v); });
+        if (at.on >> k & 1u) f(k, [&](int q, float2 v) { s[0][q] = add(s[0][q], v); });
       sum(s);
 #pragma unroll
       for (int q = 0; q < Q; ++q) neg[q] = mul(s[0][q], both(-inv));
@@ -197,7 +207,7 @@ struct Grid {
     for (int q = 0; q < Q; ++q) s[0][q] = both(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (has(k))
+      if (at.on >> k & 1u)
         f(k, [&](int q, float2 v) {
           const float2 d = add(v, neg[q]);
           s[0][q] = fma(d, d, s[0][q]);
@@ -209,18 +219,18 @@ struct Grid {
   }
 
   // y's statistics, the dropout bits and h.  Slots: 0 x, 1 y.
-  __device__ void head(bool has_y, unsigned (&keep)[K], float2 (&hv)[K][Q], float2 (&neg)[Q], float2 (&rho)[Q]) const {
+  __device__ void head(const Spot& at, bool has_y, unsigned (&keep)[K], float2 (&hv)[K][Q], float2 (&neg)[Q], float2 (&rho)[Q]) const {
     if (!has_y) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (has(k)) {
+        if (at.on >> k & 1u) {
           const uint4 x = raw(0, k);
 #pragma unroll
           for (int q = 0; q < Q; ++q) hv[k][q] = Vec<TT>::get(x, q);
         }
       return;
     }
-    stats(j.post, j.eps1, neg, rho, [&](int k, auto use) {
+    stats(at, j.post, j.eps1, neg, rho, [&](int k, auto use) {
       const uint4 y = raw(1, k);
 #pragma unroll
       for (int q = 0; q < Q; ++q) use(q, Vec<TT>::get(y, q));
@@ -229,14 +239,14 @@ struct Grid {
       const DropState ds = drop_state(j.rng);
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (has(k)) keep[k] = keep_bits<V>(ds, j.border, at(k));
+        if (at.on >> k & 1u) keep[k] = keep_bits<V>(ds, j.border, at.at + k * step);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!has(k)) continue;
+      if (!(at.on >> k & 1u)) continue;
       const uint4 x = raw(0, k), y = raw(1, k);
       const float4 cf = *HND_S(coef + chan(k));
-      const float g = gate(k) * j.factor;
+      const float g = gate(at, k) * j.factor;
       const float2 al = both(cf.x * g), be = both(cf.y * g);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
@@ -253,56 +263,51 @@ struct Grid {
 };
 
 template <class TT, int K>
-__global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w, const TT* __restrict__ x,
-                                                         const TT* __restrict__ y, TT* __restrict__ h,
-                                                         TT* __restrict__ n) {
+__global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w, Div per, int units,
+                                                         const TT* __restrict__ x, const TT* __restrict__ y,
+                                                         TT* __restrict__ h, TT* __restrict__ n) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
   using G = Grid<TT, K>;
   constexpr int Q = G::Q;
-  G t(j, w, 2, hnd_dyn_smem);
-  const long long units = t.per * j.B, tiles = (units + w - 1) / w;
-  auto place = [&](long long i) {
-    const long long u = i * w + t.lane, b = u / t.per;
-    t.place(b, u - b * t.per, u < units);
+  const G t(j, w, 2, hnd_dyn_smem);
+  // vectors of positions are counted through the samples; `per` is those of one
+  auto spot = [&](int u) {
+    const int b = per.quot(u);
+    return t.spot(b, u - b * static_cast<int>(per.d), u < units);
   };
-  place(blockIdx.x);
-  t.fetch(0, x);
-  t.fetch(1, y);
-  for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
+  const int stride = gridDim.x * w;
+  int u = blockIdx.x * w + t.lane;
+  Spot at = spot(u);
+  t.fetch(at, 0, x);
+  t.fetch(at, 1, y);
+  for (; u - t.lane < units; u += stride) {
     copies_done();
     unsigned keep[K];
     float2 hv[K][Q], neg[Q], rho[Q];
-    t.head(y != nullptr, keep, hv, neg, rho);
+    t.head(at, y != nullptr, keep, hv, neg, rho);
     // the slots are used up: on to the next tile's copies
-    const long long base = t.base, b = t.b;
-    const bool live = t.live;
-    if (i + gridDim.x < tiles) {
-      place(i + gridDim.x);
-      t.fetch(0, x);
-      t.fetch(1, y);
-    }
-    const long long next_base = t.base, next_b = t.b;
-    const bool next_live = t.live;
-    t.base = base, t.b = b, t.live = live;
+    const Spot next = spot(u + stride);
+    t.fetch(next, 0, x);
+    t.fetch(next, 1, y);
     if (h)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (t.has(k)) t.store(h, k, hv[k]);
+        if (at.on >> k & 1u) t.store(at, h, k, hv[k]);
     if (n) {
-      t.stats(j.pre, j.eps2, neg, rho, [&](int k, auto use) {
+      t.stats(at, j.pre, j.eps2, neg, rho, [&](int k, auto use) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) use(q, hv[k][q]);
       });
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!t.has(k)) continue;
+        if (!(at.on >> k & 1u)) continue;
         const float4 cf = *HND_S(t.coef + t.chan(k));
 #pragma unroll
         for (int q = 0; q < Q; ++q) hv[k][q] = fma(mul(add(hv[k][q], neg[q]), rho[q]), both(cf.z), both(cf.w));
-        t.store(n, k, hv[k]);
+        t.store(at, n, k, hv[k]);
       }
     }
-    t.base = next_base, t.b = next_b, t.live = next_live;
+    at = next;
   }
 }
 
@@ -311,42 +316,34 @@ __global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w,
 // part[block][C].
 template <class TT, int K>
 __global__ void __launch_bounds__(kT, 2)
-    k_join_grid_bwd(const JoinDev j, int w, int chunks, const TT* __restrict__ x, const TT* __restrict__ y,
+    k_join_grid_bwd(const JoinDev j, int w, int per, int chunks, const TT* __restrict__ x, const TT* __restrict__ y,
                     const TT* __restrict__ dh, const TT* __restrict__ dn, TT* __restrict__ dx, TT* __restrict__ dy,
                     float4* __restrict__ part) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
   using G = Grid<TT, K>;
   constexpr int Q = G::Q;
-  G t(j, w, 4, hnd_dyn_smem);
+  const G t(j, w, 4, hnd_dyn_smem);
   const float2 inv = both(1.f / static_cast<float>(j.C));
-  const long long tiles = (t.per + w - 1) / w, sample = blockIdx.x / chunks, first = blockIdx.x % chunks;
+  const int sample = blockIdx.x / chunks, stride = chunks * w;
   float4 acc[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto place = [&](long long i) {
-    const long long u = i * w + t.lane;
-    t.place(sample, u, u < t.per);
-  };
-  place(first);
-  t.fetch(0, x);
-  t.fetch(1, y);
-  t.fetch(2, dn);
-  t.fetch(3, dh);
-  for (long long i = first; i < tiles; i += chunks) {
+  auto spot = [&](int u) { return t.spot(sample, u, u < per); };
+  int u = (blockIdx.x - sample * chunks) * w + t.lane;
+  Spot at = spot(u);
+  t.fetch(at, 0, x);
+  t.fetch(at, 1, y);
+  t.fetch(at, 2, dn);
+  t.fetch(at, 3, dh);
+  for (; u - t.lane < per; u += stride) {
     copies_done();
-    const bool more = i + chunks < tiles;
     unsigned keep[K];
     float2 hv[K][Q], neg1[Q], rho1[Q], neg2[Q], rho2[Q];
-    t.head(y != nullptr, keep, hv, neg1, rho1);
-    auto ahead = [&](int tensor, const TT* p) {      // a used-up slot takes the next tile
-      if (!more) return;
-      place(i + chunks);
-      t.fetch(tensor, p);
-      place(i);
-    };
-    ahead(0, x);
+    t.head(at, y != nullptr, keep, hv, neg1, rho1);
+    const Spot next = spot(u + stride);      // used-up slots take the next tile
+    t.fetch(next, 0, x);
     if (dn) {
-      t.stats(j.pre, j.eps2, neg2, rho2, [&](int k, auto use) {
+      t.stats(at, j.pre, j.eps2, neg2, rho2, [&](int k, auto use) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) use(q, hv[k][q]);
       });
@@ -355,7 +352,7 @@ __global__ void __launch_bounds__(kT, 2)
       for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!t.has(k)) continue;
+        if (!(at.on >> k & 1u)) continue;
         const uint4 rn = t.raw(2, k);
         const float2 w2 = both((*HND_S(t.coef + t.chan(k))).z);
         float2 z = both(0.f), u = both(0.f);
@@ -379,7 +376,7 @@ __global__ void __launch_bounds__(kT, 2)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!t.has(k)) continue;
+        if (!(at.on >> k & 1u)) continue;
         const uint4 rn = t.raw(2, k);
         uint4 rh = make_uint4(0, 0, 0, 0);
         if (dh) rh = t.raw(3, k);
@@ -392,25 +389,25 @@ __global__ void __launch_bounds__(kT, 2)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         uint4 rh = make_uint4(0, 0, 0, 0);
-        if (dh && t.has(k)) rh = t.raw(3, k);
+        if (dh && (at.on >> k & 1u)) rh = t.raw(3, k);
 #pragma unroll
         for (int q = 0; q < Q; ++q) hv[k][q] = Vec<TT>::get(rh, q);
       }
     }
-    ahead(2, dn);
-    ahead(3, dh);
+    t.fetch(next, 2, dn);
+    t.fetch(next, 3, dh);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (t.has(k)) t.store(dx, k, hv[k]);
+      if (at.on >> k & 1u) t.store(at, dx, k, hv[k]);
     if (y) {
       float2 s[2][Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!t.has(k)) continue;
+        if (!(at.on >> k & 1u)) continue;
         const uint4 ry = t.raw(1, k);
-        const float2 al = both((*HND_S(t.coef + t.chan(k))).x * t.gate(k));
+        const float2 al = both((*HND_S(t.coef + t.chan(k))).x * t.gate(at, k));
         float2 a = both(0.f), r = both(0.f);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -439,7 +436,7 @@ __global__ void __launch_bounds__(kT, 2)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!t.has(k)) continue;
+        if (!(at.on >> k & 1u)) continue;
         if (j.post) {
           const uint4 ry = t.raw(1, k);
 #pragma unroll
@@ -448,14 +445,13 @@ __global__ void __launch_bounds__(kT, 2)
             hv[k][q] = mul(rho1[q], fma(yh, s[1][q], add(hv[k][q], s[0][q])));
           }
         }
-        t.store(dy, k, hv[k]);
+        t.store(at, dy, k, hv[k]);
       }
-      ahead(1, y);
+      t.fetch(next, 1, y);
     }
-    if (more) place(i + chunks);
+    at = next;
   }
   if (!part) return;
-  t.live = true;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float4 s = acc[k];
@@ -465,7 +461,7 @@ __global__ void __launch_bounds__(kT, 2)
       s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
       s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, o);
     }
-    if (t.has(k) && t.lane == 0) *HND_G(part + blockIdx.x * j.C + t.chan(k)) = s;
+    if ((t.chans >> k & 1u) && t.lane == 0) *HND_G(part + blockIdx.x * j.C + t.chan(k)) = s;
   }
 }
 

@@ -10,8 +10,9 @@ static cudaError_t fwd(const JoinArgs& a, const JoinDev& j, int w, unsigned bloc
   const size_t smem = grid::smem_bytes(2, K, a.C, w, 16 / sizeof(TT));
   const cudaError_t e = ensure_smem(kern, grid::smem_bytes(2, K, 2048, 32, 16 / sizeof(TT)));
   if (e != cudaSuccess) return e;
-  kern<<<blocks, grid::kT, smem, a.stream>>>(j, w, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y),
-                                             static_cast<TT*>(a.h), static_cast<TT*>(a.n));
+  const long long per = a.L * sizeof(TT) / 16;
+  kern<<<blocks, grid::kT, smem, a.stream>>>(j, w, make_div(static_cast<uint32_t>(per)), static_cast<int>(per * a.B),
+                                             static_cast<const TT*>(a.x), static_cast<const TT*>(a.y), static_cast<TT*>(a.h), static_cast<TT*>(a.n));
   return cudaGetLastError();
 }
 
@@ -21,7 +22,7 @@ static cudaError_t bwd(const JoinArgs& a, const JoinDev& j, int w, int chunks, u
   const size_t smem = grid::smem_bytes(4, K, a.C, w, 16 / sizeof(TT));
   const cudaError_t e = ensure_smem(kern, grid::smem_bytes(4, K, 2048, 32, 16 / sizeof(TT)));
   if (e != cudaSuccess) return e;
-  kern<<<blocks, grid::kT, smem, a.stream>>>(j, w, chunks, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y),
+  kern<<<blocks, grid::kT, smem, a.stream>>>(j, w, static_cast<int>(a.L * sizeof(TT) / 16), chunks, static_cast<const TT*>(a.x), static_cast<const TT*>(a.y),
                                              static_cast<const TT*>(a.dh), static_cast<const TT*>(a.dn),
                                              static_cast<TT*>(a.dx), static_cast<TT*>(a.dy), part);
   return cudaGetLastError();

@@ -13,6 +13,14 @@
 //
 // W neighbouring lanes hold 16 bytes of positions each, the rest of the 256
 // threads the channels, K apiece.
+//
+// Rows that do not start on 16 bytes (RAG) come as the aligned vectors that
+// cover them, one more than the lanes, and every thread shifts its positions
+// out of its own and the next one's; on the way out it shifts them back with
+// the lane before, so that all but a row's first and last vector leave whole.
+// Eight elements then take two counters of the generator; the second is the
+// next lane's first.  (One value a thread and load, as hnd_join.cuh does it for
+// such rows, took 107 us for 13 x 204 x 777 bf16 forward and backward.)
 #pragma once
 
 #include "hnd_div.cuh"
@@ -77,37 +85,87 @@ struct Vec<float> {
   }
 };
 
-__device__ __forceinline__ void copy16(uint4* slot, const void* src) {
-  if (HND_RANGE_OK(src, 16))
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
-                 "l"(src)
+// 16 bytes, or the first `bytes` of them and zeros.
+__device__ __forceinline__ void copy16(uint4* slot, const void* src, int bytes = 16) {
+  if (HND_RANGE_OK(src, bytes))
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+                 "l"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void copies_done() {
   asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
 }
 
-// Shared memory: slots [tensor][K][kT] of 16 bytes, factors [C], sums.
-inline size_t smem_bytes(int tensors, int K, long long C, int w, int V) {
-  return static_cast<size_t>(tensors) * K * kT * 16 + static_cast<size_t>(C) * 16 + sizeof(float) * (kWarps + 1) * 2 * w * V;
+// Elements n .. n + V - 1 of a and b one after the other (0 <= n < V).
+template <class TT>
+__device__ __forceinline__ uint4 funnel(const uint4& a, const uint4& b, unsigned n) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const unsigned words = sizeof(TT) == 2 ? n >> 1 : n;
+  if (words & 2)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (words & 1)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if constexpr (sizeof(TT) == 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (n & 1) * 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The first n elements, and zeros.
+template <class TT>
+__device__ __forceinline__ uint4 first(const uint4& a, int n) {
+  uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if constexpr (sizeof(TT) == 2)
+      w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xFFFFu : 0u;
+    else
+      w[i] = i < n ? w[i] : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Elements lo .. hi - 1 one by one.
+template <class TT>
+__device__ __forceinline__ void put_some(TT* p, const uint4& a, int lo, int hi) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(16 / sizeof(TT)); ++i)
+    if (i >= lo && i < hi) {
+      if constexpr (sizeof(TT) == 2)
+        *HND_G(reinterpret_cast<unsigned short*>(p) + i) = static_cast<unsigned short>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      else
+        *HND_G(reinterpret_cast<unsigned*>(p) + i) = w[i];
+    }
 }
 
-// Where a thread's vectors of a tile lie: its first element, its sample, and a
-// bit for each of its channels that is there.
+// Shared memory: slots [tensor][K][rows][w, and one more if ragged] of 16
+// bytes, factors [C], sums.
+inline size_t smem_bytes(int tensors, int K, long long C, int w, int V, bool ragged) {
+  return static_cast<size_t>(tensors) * K * (kT + (ragged ? kT / w : 0)) * 16 + static_cast<size_t>(C) * 16 +
+         sizeof(float) * (kWarps + 1) * 2 * w * V;
+}
+
+// Where a thread's vectors of a tile lie: its first element, its sample, a bit
+// for each of its channels that is there, and how many of its positions are
+// (ragged: and whether the next lane has some).
 struct Spot {
   long long at;
   int b;
   unsigned on;
+  int n;
+  bool next;
 };
 
-template <class TT, int K>
+template <class TT, int K, bool RAG>
 struct Grid {
   static constexpr int Q = Vec<TT>::Q, V = 2 * Q;
   const JoinDev& j;
   const int w, lane, cg, rows, C;
   unsigned chans = 0;               // bit k: channel k of the thread exists
   long long own, step;              // of its first channel in a sample, and from one of its channels to the next
-  uint4* slots;
+  uint4* slots;                     // its own
+  int pitch;                        // slots from one k to the next
   float4* coef;                     // of a channel: scale w1, scale b1, w2, b2
   float* part;                      // [kWarps][2 V w]
   float* total;                     // [2 V w]
@@ -118,8 +176,9 @@ struct Grid {
     for (int k = 0; k < K; ++k) chans |= static_cast<unsigned>(chan(k) < C) << k;
     own = cg * j.L;
     step = rows * j.L;
-    slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;
-    coef = reinterpret_cast<float4*>(reinterpret_cast<uint4*>(smem) + tensors * K * kT);
+    pitch = kT + (RAG ? rows : 0);
+    slots = reinterpret_cast<uint4*>(smem) + cg * (w + RAG) + lane;
+    coef = reinterpret_cast<float4*>(reinterpret_cast<uint4*>(smem) + tensors * K * pitch);
     part = reinterpret_cast<float*>(coef + C);
     total = part + kWarps * 2 * V * w;
     for (int c = threadIdx.x; c < C; c += kT) {
@@ -130,23 +189,148 @@ struct Grid {
     __syncthreads();
   }
   __device__ int chan(int k) const { return cg + k * rows; }
-  __device__ uint4 raw(int tensor, int k) const { return *HND_S(slots + (tensor * K + k) * kT); }
+  __device__ uint4 raw(int tensor, int k) const { return *HND_S(slots + (tensor * K + k) * pitch); }
   __device__ float gate(const Spot& s, int k) const {
     return j.gate ? __ldg(HND_G(j.gate + static_cast<long long>(s.b) * C + chan(k))) : 1.f;
   }
-  // Vector u of sample b.
-  __device__ Spot spot(int b, int u, bool live) const {
-    return Spot{live ? b * j.C * j.L + static_cast<long long>(u) * V + own : 0, live ? b : 0, live ? chans : 0u};
+  // Vector u of sample b, `left` positions of the sample from there on.
+  __device__ Spot spot(int b, int u, int left) const {
+    const bool live = left > 0;
+    return Spot{b * j.C * j.L + static_cast<long long>(u) * V + own, live ? b : 0, live ? chans : 0u,
+                live ? min(left, V) : 0, RAG && lane + 1 < w && left > V};
   }
   __device__ void fetch(const Spot& s, int tensor, const TT* p) const {
     if (!p) return;
-    const TT* from = p + s.at;
+    if constexpr (RAG) {
+      __syncwarp();      // the slot after the lane's own is another lane's
+      const long long all = j.T * j.C;
 #pragma unroll
-    for (int k = 0; k < K; ++k, from += step)
-      if (s.on >> k & 1u) copy16(slots + (tensor * K + k) * kT, from);
+      for (int k = 0; k < K; ++k) {
+        if (!(s.on >> k & 1u)) continue;
+        const long long e = s.at + k * step;
+        const int shift = static_cast<int>(e & (V - 1));
+        const long long from = e - shift, rest = (all - from) * static_cast<int>(sizeof(TT));
+        uint4* slot = slots + (tensor * K + k) * pitch;
+        copy16(slot, p + from, rest < 16 ? static_cast<int>(rest) : 16);
+        if (!s.next && shift + s.n > V)
+          copy16(slot + 1, p + from + V, rest < 32 ? static_cast<int>(rest) - 16 : 16);
+      }
+    } else {
+      const TT* from = p + s.at;
+#pragma unroll
+      for (int k = 0; k < K; ++k, from += step)
+        if (s.on >> k & 1u) copy16(slots + (tensor * K + k) * pitch, from);
+    }
   }
+  // Ragged: the lane's own positions out of the aligned vectors, zeros behind
+  // the row's end, back into its slots.
+  __device__ void align(const Spot& s, int tensor) const {
+    if constexpr (RAG) {
+      uint4 v[K];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint4* slot = slots + (tensor * K + k) * pitch;
+        v[k] = funnel<TT>(*HND_S(slot), *HND_S(slot + 1), static_cast<unsigned>(s.at + k * step) & (V - 1));
+        if (s.n < V) v[k] = first<TT>(v[k], s.n);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < K; ++k) *HND_S(slots + (tensor * K + k) * pitch) = v[k];
+    }
+  }
+  // All lanes of a warp take part, for each k.
   __device__ void store(const Spot& s, TT* p, int k, const float2 (&f)[Q]) const {
-    __stcs(HND_G(reinterpret_cast<uint4*>(p + (s.at + k * step))), Vec<TT>::put(f));
+    const bool on = s.on >> k & 1u;
+    const long long e = s.at + k * step;
+    const uint4 mine = Vec<TT>::put(f);
+    if constexpr (RAG) {
+      const int shift = static_cast<int>(e & (V - 1));
+      uint4 before;
+      before.x = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1, w);
+      before.y = __shfl_up_sync(0xFFFFFFFFu, mine.y, 1, w);
+      before.z = __shfl_up_sync(0xFFFFFFFFu, mine.z, 1, w);
+      before.w = __shfl_up_sync(0xFFFFFFFFu, mine.w, 1, w);
+      // the vector that the lane's first position lies in, and what spills into the one after it
+      const uint4 head = shift ? funnel<TT>(before, mine, V - shift) : mine;
+      const int lo = lane ? 0 : shift, hi = min(V, shift + s.n), spill = s.next ? 0 : shift + s.n - V;
+      TT* to = p + (e - shift);
+      const bool whole = on && lo == 0 && hi == V, some = on && !whole, over = on && spill > 0;
+      if (whole) __stcs(HND_G(reinterpret_cast<uint4*>(to)), head);
+      const uint4 tail = shift ? funnel<TT>(mine, mine, V - shift) : mine;
+      // a row's first vector by one lane and its spill by another, in one go
+      if (some) {
+        put_some(to, head, lo, hi);
+      } else if (over) {
+        put_some(to + V, tail, 0, spill);
+      }
+      if (some && over) put_some(to + V, tail, 0, spill);
+      __syncwarp();
+    } else {
+      if (on) __stcs(HND_G(reinterpret_cast<uint4*>(p + e)), mine);
+    }
+  }
+
+  // The eight mask bits of a group.
+  __device__ unsigned group_bits(const DropState& ds, long long group) const {
+    const uint4 v = drop_lots(ds, static_cast<uint64_t>(group));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    unsigned bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bits |= static_cast<unsigned>((u[i] & 0xFFFFu) >= j.border) << (2 * i) |
+              static_cast<unsigned>((u[i] >> 16) >= j.border) << (2 * i + 1);
+    return bits;
+  }
+  // keep[k]: a bit for each of the lane's positions.  All lanes take part.
+  __device__ void mask(const Spot& s, unsigned (&keep)[K]) const {
+    const DropState ds = drop_state(j.rng);
+    if constexpr (V == 8 && !RAG) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) keep[k] = group_bits(ds, (s.at + k * step) >> 3);
+    } else if constexpr (V == 8) {
+      // lane i has group i of the row's tile; of the group behind the last lane's, lane q takes channel q / rows of a
+      // warp in row q % rows
+      const int rw = 32 / w, q = threadIdx.x & 31, row = q / w;
+#pragma unroll
+      for (int k = 0; k < K; ++k) keep[k] = group_bits(ds, (s.at + k * step) >> 3);
+      unsigned behind[K];
+      for (int done = 0; done < K * rw; done += 32) {
+        const int k = (done + q) / rw, r = (done + q) % rw;
+        const long long at0 = __shfl_sync(0xFFFFFFFFu, s.at, r * w + w - 1);      // of that row's last lane
+        const unsigned got = k < K ? group_bits(ds, ((at0 + k * step) >> 3) + 1) : 0u;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const int from = i * rw + row - done;
+          const unsigned v = __shfl_sync(0xFFFFFFFFu, got, from & 31);
+          if (from >= 0 && from < 32) behind[i] = v;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        unsigned after = __shfl_down_sync(0xFFFFFFFFu, keep[k], 1, w);
+        if (lane == w - 1) after = behind[k];
+        keep[k] = (keep[k] | after << 8) >> (static_cast<unsigned>(s.at + k * step) & 7);
+      }
+    } else if (!RAG && K % 2 == 0 && w > 1 && j.L % 8 == 0) {
+      // two lanes lie in one group: each takes one channel of two
+      const int odd = lane & 1;
+#pragma unroll
+      for (int k = 0; k + 1 < K; k += 2) {
+        const unsigned mine = group_bits(ds, (s.at + (k + odd) * step) >> 3);
+        const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+        keep[k] = (odd ? other : mine) >> (4 * odd);
+        keep[k + 1] = (odd ? mine : other) >> (4 * odd);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const long long e = s.at + k * step;
+        unsigned bits = group_bits(ds, e >> 3);
+        if (RAG && (e & 7) > 4) bits |= group_bits(ds, (e >> 3) + 1) << 8;
+        keep[k] = bits >> (e & 7);
+      }
+    }
   }
 
   // Sums over the channels of N values at each of the thread's positions:
@@ -235,12 +419,7 @@ struct Grid {
 #pragma unroll
       for (int q = 0; q < Q; ++q) use(q, Vec<TT>::get(y, q));
     });
-    if (j.border) {
-      const DropState ds = drop_state(j.rng);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (at.on >> k & 1u) keep[k] = keep_bits<V>(ds, j.border, at.at + k * step);
-    }
+    if (j.border) mask(at, keep);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (!(at.on >> k & 1u)) continue;
@@ -262,37 +441,41 @@ struct Grid {
   }
 };
 
-template <class TT, int K>
+template <class TT, int K, bool RAG>
 __global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w, Div per, int units,
                                                          const TT* __restrict__ x, const TT* __restrict__ y,
                                                          TT* __restrict__ h, TT* __restrict__ n) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
-  using G = Grid<TT, K>;
+  using G = Grid<TT, K, RAG>;
   constexpr int Q = G::Q;
   const G t(j, w, 2, hnd_dyn_smem);
-  // vectors of positions are counted through the samples; `per` is those of one
-  auto spot = [&](int u) {
-    const int b = per.quot(u);
-    return t.spot(b, u - b * static_cast<int>(per.d), u < units);
+  // Vectors of positions are counted through the samples, `per` to each, and a
+  // tile takes w of them; ragged, a tile keeps to one sample and `per` counts
+  // its tiles.
+  auto spot = [&](int i) {
+    const int u = RAG ? i : i * w + t.lane, b = per.quot(min(u, units - 1)), v = u - b * static_cast<int>(per.d);
+    const int from = RAG ? v * w + t.lane : v;
+    return t.spot(b, from, u < units ? static_cast<int>(min(j.L - static_cast<long long>(from) * G::V, 1LL << 30)) : 0);
   };
-  const int stride = gridDim.x * w;
-  int u = blockIdx.x * w + t.lane;
-  Spot at = spot(u);
+  const int tiles = RAG ? units : (units + w - 1) / w;
+  Spot at = spot(blockIdx.x);
   t.fetch(at, 0, x);
   t.fetch(at, 1, y);
-  for (; u - t.lane < units; u += stride) {
+  for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
     copies_done();
+    t.align(at, 0);
+    if (y) t.align(at, 1);
     unsigned keep[K];
     float2 hv[K][Q], neg[Q], rho[Q];
     t.head(at, y != nullptr, keep, hv, neg, rho);
     // the slots are used up: on to the next tile's copies
-    const Spot next = spot(u + stride);
+    const Spot next = spot(min(i + static_cast<int>(gridDim.x), tiles));
     t.fetch(next, 0, x);
     t.fetch(next, 1, y);
     if (h)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (at.on >> k & 1u) t.store(at, h, k, hv[k]);
+        t.store(at, h, k, hv[k]);
     if (n) {
       t.stats(at, j.pre, j.eps2, neg, rho, [&](int k, auto use) {
 #pragma unroll
@@ -300,10 +483,11 @@ __global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w,
       });
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!(at.on >> k & 1u)) continue;
-        const float4 cf = *HND_S(t.coef + t.chan(k));
+        if (at.on >> k & 1u) {
+          const float4 cf = *HND_S(t.coef + t.chan(k));
 #pragma unroll
-        for (int q = 0; q < Q; ++q) hv[k][q] = fma(mul(add(hv[k][q], neg[q]), rho[q]), both(cf.z), both(cf.w));
+          for (int q = 0; q < Q; ++q) hv[k][q] = fma(mul(add(hv[k][q], neg[q]), rho[q]), both(cf.z), both(cf.w));
+        }
         t.store(at, n, k, hv[k]);
       }
     }
@@ -314,13 +498,13 @@ __global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w,
 // Gradients: a block goes through the tiles of its chunk of a sample and
 // leaves each channel's sums of dht m yhat, dht m, dn hhat and dn in
 // part[block][C].
-template <class TT, int K>
+template <class TT, int K, bool RAG>
 __global__ void __launch_bounds__(kT, 2)
     k_join_grid_bwd(const JoinDev j, int w, int per, int chunks, const TT* __restrict__ x, const TT* __restrict__ y,
                     const TT* __restrict__ dh, const TT* __restrict__ dn, TT* __restrict__ dx, TT* __restrict__ dy,
                     float4* __restrict__ part) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
-  using G = Grid<TT, K>;
+  using G = Grid<TT, K, RAG>;
   constexpr int Q = G::Q;
   const G t(j, w, 4, hnd_dyn_smem);
   const float2 inv = both(1.f / static_cast<float>(j.C));
@@ -328,7 +512,9 @@ __global__ void __launch_bounds__(kT, 2)
   float4 acc[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto spot = [&](int u) { return t.spot(sample, u, u < per); };
+  auto spot = [&](int u) {
+    return t.spot(sample, min(u, per), static_cast<int>(min(j.L - static_cast<long long>(min(u, per)) * G::V, 1LL << 30)));
+  };
   int u = (blockIdx.x - sample * chunks) * w + t.lane;
   Spot at = spot(u);
   t.fetch(at, 0, x);
@@ -337,6 +523,10 @@ __global__ void __launch_bounds__(kT, 2)
   t.fetch(at, 3, dh);
   for (; u - t.lane < per; u += stride) {
     copies_done();
+    t.align(at, 0);
+    if (y) t.align(at, 1);
+    if (dn) t.align(at, 2);
+    if (dh) t.align(at, 3);
     unsigned keep[K];
     float2 hv[K][Q], neg1[Q], rho1[Q], neg2[Q], rho2[Q];
     t.head(at, y != nullptr, keep, hv, neg1, rho1);
@@ -398,7 +588,7 @@ __global__ void __launch_bounds__(kT, 2)
     t.fetch(next, 3, dh);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (at.on >> k & 1u) t.store(at, dx, k, hv[k]);
+      t.store(at, dx, k, hv[k]);
     if (y) {
       float2 s[2][Q];
 #pragma unroll
@@ -436,8 +626,7 @@ __global__ void __launch_bounds__(kT, 2)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!(at.on >> k & 1u)) continue;
-        if (j.post) {
+        if (j.post && (at.on >> k & 1u)) {
           const uint4 ry = t.raw(1, k);
 #pragma unroll
           for (int q = 0; q < Q; ++q) {

@@ -304,16 +304,17 @@ static bool grid_plan(JoinPlan& p, long long C, long long units, int widest) {
   return false;
 }
 
-// Aligned grids of up to 512 channels (bf16 forward; 1024 and 512 of fp32):
-// as many lanes of positions as leave threads for the channels.
+// Grids of up to 512 channels (fp32 forward 1024): as many lanes of positions
+// as leave threads for the channels, two at least where a row has two vectors.
 static bool ahead_plan(JoinPlan& p, long long B, long long C, long long L, int bf16, bool backward) {
   const int V = bf16 ? 8 : 4, most = backward || bf16 ? 4 : 8;
-  if (L == 1 || L % V) return false;
-  const long long per = L / V, units = backward ? per : per * B;
+  if (L == 1) return false;
+  const bool ragged = L % V != 0;
+  const long long per = cdiv(L, V), units = backward || ragged ? per : per * B;
   p.K = C <= 32 ? 1 : most;
   int w = 32;
-  while (w > 2 && (256 / w * p.K < C || w / 2 >= units)) w /= 2;
-  if (256 / w * p.K < C) return false;
+  while (w > 1 && (256 / w * p.K < C || w / 2 >= units)) w /= 2;
+  if (256 / w * p.K < C || (w == 1 && units > 1)) return false;
   p.V = V;
   p.lanes = w;
   const long long tiles = cdiv(units, w);
@@ -322,7 +323,8 @@ static bool ahead_plan(JoinPlan& p, long long B, long long C, long long L, int b
     p.chunks = static_cast<int>(tiles < want ? tiles : want);
     p.blocks = p.rows = B * p.chunks;
   } else {
-    p.blocks = tiles < 444 ? tiles : 444;                                    // three an SM
+    const long long all = ragged ? tiles * B : tiles;
+    p.blocks = all < 444 ? all : 444;                                        // three an SM
   }
   p.fast = p.ahead = true;
   return true;

@@ -150,6 +150,27 @@ JOIN = [
     ((3,), 1, 9000, "f32", "rms", "rms", "wbgs", 0.1),
     ((8,), 1, 65536, "bf16", "rms", "layer", "wgs", 0.0),        # the most channels
     ((8,), 1200, 16, "f32", "layer", "rms", "wbgs", 0.1),        # many short samples
+    # rows of 16 bytes: one to many lanes of positions, channels that fill a block or not
+    ((24,), 2, 300, "bf16", "layer", "rms", "wbgs", 0.1),
+    ((40,), 2, 700, "f32", "rms", "layer", "wbgs", 0.1),
+    ((12,), 3, 40, "f32", "layer", "layer", "wbgs", 0.3),        # rows of half a counter group
+    ((16, 128), 3, 9, "bf16", "rms", "layer", "wbgs", 0.3),
+    ((1024,), 1, 256, "f32", "layer", "rms", "wbgs", 0.3),
+    ((512,), 5, 512, "bf16", "rms", "rms", "wgs", 0.1),
+    # rows that start anywhere: every shift, short and long, a last vector of each length
+    ((2,), 9, 30, "bf16", "layer", "rms", "wbgs", 0.4),
+    ((3,), 5, 700, "f32", "rms", "layer", "wbgs", 0.4),
+    ((5,), 4, 1000, "f32", "layer", "rms", "wbgs", 0.2),
+    ((7,), 40, 70, "bf16", "rms", "layer", "wbgs", 0.2),
+    ((9,), 2, 500, "bf16", "layer", "layer", "wbgs", 0.2),
+    ((11,), 3, 129, "f32", "layer", "layer", "wbgs", 0.2),
+    ((255,), 1, 129, "f32", "rms", "rms", "wbgs", 0.2),
+    ((257,), 2, 40, "bf16", "layer", "rms", "wbgs", 0.2),
+    ((1003,), 2, 7, "bf16", "rms", "layer", "wbgs", 0.5),
+    ((4097,), 1, 33, "f32", "layer", "rms", "wbgs", 0.5),
+    ((31, 33), 2, 512, "bf16", "rms", "layer", "gs", 0.1),
+    ((6,), 3, 2000, "f32", "rms", "rms", "wbgs", 0.1),
+    ((4,), 3, 900, "bf16", "layer", "layer", "wbgs", 0.1),
 ]
 
 
@@ -158,6 +179,21 @@ def test_join_parity(dims, B, C, dt, post, pre, params, p):
     c = JoinCase(dims, B, C, dt, post, pre, params, p)
     c.check_forward()
     c.check_backward()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("dims,C", [((13,), 24), ((8, 8), 64), ((777,), 9)])
+def test_join_writes_its_outputs_only(dims, C, dt):
+    """Outputs in the middle of larger buffers: what lies before and behind stays as it was."""
+    t = torch()
+    c = JoinCase(dims, 2, C, dt, "rms", "layer", "wbgs", 0.2)
+    want_h, want_n = c.op(c.t["x"], c.t["y"], rng=c.rng)
+    size, pad = want_h.numel(), 64
+    h, n = (t.full((size + 2 * pad,), 7.0, dtype=want_h.dtype, device="cuda") for _ in range(2))
+    c.op(c.t["x"], c.t["y"], rng=c.rng, h=h[pad:pad + size].view(want_h.shape), n=n[pad:pad + size].view(want_h.shape))
+    for buf, want in ((h, want_h), (n, want_n)):
+        assert t.equal(buf[pad:pad + size].view(want.shape), want)
+        assert (buf[:pad] == 7).all() and (buf[pad + size:] == 7).all()
 
 
 @pytest.mark.parametrize("dims,C", [((1,), 64), ((8, 8), 64), ((13,), 30)])

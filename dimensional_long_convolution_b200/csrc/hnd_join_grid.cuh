@@ -125,13 +125,13 @@ __device__ __forceinline__ uint4 first(const uint4& a, int n) {
       w[i] = i < n ? w[i] : 0u;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Elements lo .. hi - 1 one by one.
+// The elements whose bits are set, one by one.
 template <class TT>
-__device__ __forceinline__ void put_some(TT* p, const uint4& a, int lo, int hi) {
+__device__ __forceinline__ void put_some(TT* p, const uint4& a, unsigned bits) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < static_cast<int>(16 / sizeof(TT)); ++i)
-    if (i >= lo && i < hi) {
+    if (bits >> i & 1u) {
       if constexpr (sizeof(TT) == 2)
         *HND_G(reinterpret_cast<unsigned short*>(p) + i) = static_cast<unsigned short>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
       else
@@ -193,6 +193,10 @@ struct Grid {
   __device__ float gate(const Spot& s, int k) const {
     return j.gate ? __ldg(HND_G(j.gate + static_cast<long long>(s.b) * C + chan(k))) : 1.f;
   }
+  // Ragged: how far into its aligned vector the lane's first position lies.
+  __device__ int shift(const Spot& s, int k) const {
+    return static_cast<int>((static_cast<unsigned>(s.at) + k * static_cast<unsigned>(step)) & (V - 1));
+  }
   // Vector u of sample b, `left` positions of the sample from there on.
   __device__ Spot spot(int b, int u, int left) const {
     const bool live = left > 0;
@@ -207,12 +211,11 @@ struct Grid {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (!(s.on >> k & 1u)) continue;
-        const long long e = s.at + k * step;
-        const int shift = static_cast<int>(e & (V - 1));
-        const long long from = e - shift, rest = (all - from) * static_cast<int>(sizeof(TT));
+        const int in = shift(s, k);
+        const long long from = s.at + k * step - in, rest = (all - from) * static_cast<int>(sizeof(TT));
         uint4* slot = slots + (tensor * K + k) * pitch;
         copy16(slot, p + from, rest < 16 ? static_cast<int>(rest) : 16);
-        if (!s.next && shift + s.n > V)
+        if (!s.next && in + s.n > V)
           copy16(slot + 1, p + from + V, rest < 32 ? static_cast<int>(rest) - 16 : 16);
       }
     } else {
@@ -231,7 +234,7 @@ struct Grid {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const uint4* slot = slots + (tensor * K + k) * pitch;
-        v[k] = funnel<TT>(*HND_S(slot), *HND_S(slot + 1), static_cast<unsigned>(s.at + k * step) & (V - 1));
+        v[k] = funnel<TT>(*HND_S(slot), *HND_S(slot + 1), shift(s, k));
         if (s.n < V) v[k] = first<TT>(v[k], s.n);
       }
       __syncwarp();
@@ -245,27 +248,26 @@ struct Grid {
     const long long e = s.at + k * step;
     const uint4 mine = Vec<TT>::put(f);
     if constexpr (RAG) {
-      const int shift = static_cast<int>(e & (V - 1));
+      const int at = shift(s, k);
       uint4 before;
       before.x = __shfl_up_sync(0xFFFFFFFFu, mine.x, 1, w);
       before.y = __shfl_up_sync(0xFFFFFFFFu, mine.y, 1, w);
       before.z = __shfl_up_sync(0xFFFFFFFFu, mine.z, 1, w);
       before.w = __shfl_up_sync(0xFFFFFFFFu, mine.w, 1, w);
       // the vector that the lane's first position lies in, and what spills into the one after it
-      const uint4 head = shift ? funnel<TT>(before, mine, V - shift) : mine;
-      const int lo = lane ? 0 : shift, hi = min(V, shift + s.n), spill = s.next ? 0 : shift + s.n - V;
-      TT* to = p + (e - shift);
-      const bool whole = on && lo == 0 && hi == V, some = on && !whole, over = on && spill > 0;
-      if (whole) __stcs(HND_G(reinterpret_cast<uint4*>(to)), head);
-      const uint4 tail = shift ? funnel<TT>(mine, mine, V - shift) : mine;
-      // a row's first vector by one lane and its spill by another, in one go
-      if (some) {
-        put_some(to, head, lo, hi);
-      } else if (over) {
-        put_some(to + V, tail, 0, spill);
+      const uint4 head = at ? funnel<TT>(before, mine, V - at) : mine;
+      TT* to = p + (e - at);
+      unsigned some = on ? (2u << min(V, at + s.n) - 1) - (lane ? 1u : 1u << at) : 0u;
+      if (some == (1u << V) - 1) {
+        __stcs(HND_G(reinterpret_cast<uint4*>(to)), head);
+        some = 0;
       }
-      if (some && over) put_some(to + V, tail, 0, spill);
-      __syncwarp();
+      // a row's first vector by one lane and its spill by another, in one go
+      const unsigned over = on && !s.next && at + s.n > V ? (1u << (at + s.n - V)) - 1 : 0u;
+      const uint4 tail = funnel<TT>(mine, mine, (V - at) & (V - 1));
+      const bool spills = over && !some;
+      put_some(spills ? to + V : to, spills ? tail : head, spills ? over : some);
+      if (__any_sync(0xFFFFFFFFu, over && some)) put_some(to + V, tail, over && some ? over : 0u);
     } else {
       if (on) __stcs(HND_G(reinterpret_cast<uint4*>(p + e)), mine);
     }
@@ -310,7 +312,7 @@ struct Grid {
       for (int k = 0; k < K; ++k) {
         unsigned after = __shfl_down_sync(0xFFFFFFFFu, keep[k], 1, w);
         if (lane == w - 1) after = behind[k];
-        keep[k] = (keep[k] | after << 8) >> (static_cast<unsigned>(s.at + k * step) & 7);
+        keep[k] = (keep[k] | after << 8) >> shift(s, k);
       }
     } else if (!RAG && K % 2 == 0 && w > 1 && j.L % 8 == 0) {
       // two lanes lie in one group: each takes one channel of two
@@ -442,7 +444,7 @@ struct Grid {
 };
 
 template <class TT, int K, bool RAG>
-__global__ void __launch_bounds__(kT, 3) k_join_grid_fwd(const JoinDev j, int w, Div per, int units,
+__global__ void __launch_bounds__(kT, RAG ? 2 : 3) k_join_grid_fwd(const JoinDev j, int w, Div per, int units,
                                                          const TT* __restrict__ x, const TT* __restrict__ y,
                                                          TT* __restrict__ h, TT* __restrict__ n) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];

@@ -319,12 +319,17 @@ static bool ahead_plan(JoinPlan& p, long long B, long long C, long long L, int b
   p.lanes = w;
   const long long tiles = cdiv(units, w);
   if (backward) {
-    const long long want = B < kJoinParts / 2 ? kJoinParts / 2 / B : 1;      // two blocks an SM, in one wave
-    p.chunks = static_cast<int>(tiles < want ? tiles : want);
+    // two blocks an SM: one wave of few samples, or the fullest waves of many
+    const long long wave = kJoinParts / 2;
+    long long chunks = B < wave ? wave / B : 1;
+    for (long long c = chunks + 1; 2 * B > wave && c <= 8; ++c)
+      if (c * cdiv(chunks * B, wave) > chunks * cdiv(c * B, wave)) chunks = c;
+    p.chunks = static_cast<int>(tiles < chunks ? tiles : chunks);
     p.blocks = p.rows = B * p.chunks;
   } else {
     const long long all = ragged ? tiles * B : tiles;
-    p.blocks = all < 444 ? all : 444;                                        // three an SM
+    const long long most_blocks = ragged ? kJoinParts / 2 : 3 * kJoinParts / 4;      // two or three an SM
+    p.blocks = all < most_blocks ? all : most_blocks;
   }
   p.fast = p.ahead = true;
   return true;

@@ -1,6 +1,7 @@
 // The gated feed-forward block over the channels of each position: operand
 // layouts, the sequence of products, and the small kernels around them.
 #include "hnd_block.h"
+#include "hnd_ffn_few.cuh"
 #include "hnd_ffn_gemm.cuh"
 #include "hnd_host_util.h"
 #include "hnd_io.cuh"
@@ -42,6 +43,24 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// A few positions of [B, C, L] as token-major rows [plane][T][C].
+template <class TT>
+__global__ void __launch_bounds__(256)
+    k_ffn_gather(const TT* __restrict__ x, bf16* __restrict__ out, int C, int L, int T, long long plane) {
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < T * C; i += gridDim.x * 256) {
+    const int t = i / C, c = i % C;
+    const float f = ld1(x + (static_cast<long long>(t / L) * C + c) * L + t % L);
+    if constexpr (sizeof(TT) == 4) {
+      bf16 v[3];
+      split3(f, v[0], v[1], v[2]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *HND_G(out + k * plane + i) = v[k];
+    } else {
+      st1(out + i, f);
+    }
+  }
+}
+
 // The sum of a weight gradient's partial products, in the order of the splits.
 template <class TT>
 __global__ void __launch_bounds__(256)
@@ -64,6 +83,7 @@ constexpr int kPairs = 74;   // CTA pairs of a B200
 
 // Where everything lies in the workspace, a function of the descriptor alone.
 struct Layout {
+  bool few;                  // forward of a few positions: hnd_ffn_few.cuh, operands token-major
   bool token, packed;        // token-major operands; samples gathered into rows of all positions
   int planes;
   long long batches, Lx;     // of the position axis as the products see it
@@ -95,6 +115,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   const long long T = a.B * a.L;
   l.planes = a.bf16 ? 1 : 3;
   l.token = a.L == 1;
+  l.few = !backward && T <= kFewMost;
   // A row of positions has to start on 16 bytes for TMA, and a sample's last
   // tile of 256 positions should not be mostly empty: gathering costs one
   // pass over the activations, an empty half tile half the products.
@@ -111,6 +132,14 @@ static Layout layout(const FfnArgs& a, bool backward) {
     at += (static_cast<size_t>(elements) * size + 255) / 256 * 256;
     return here;
   };
+  if (l.few) {      // activations gathered token-major unless they lie so, weights as they are
+    l.act_plane = T * a.C;
+    l.hid_plane = T * a.F;
+    if (!l.token || !a.bf16) l.x = take(l.planes * l.act_plane, 2);
+    l.hid = take(l.planes * l.hid_plane, 2);
+    l.bytes = at;
+    return l;
+  }
   l.act_plane = l.token ? T * a.C : a.C * l.pitch;
   l.w_plane = a.C * a.F;
   l.hid_plane = l.batches * l.Lx * l.hpitch;
@@ -211,6 +240,49 @@ static cudaError_t run(Launch& l, cudaStream_t st) {
   if (pairs > tiles) pairs = tiles;
   kern<<<static_cast<unsigned>(2 * pairs), kThreads, smem, st>>>(l.p);
   return cudaGetLastError();
+}
+
+template <bool F32, int NT, bool DUAL>
+static cudaError_t run_few(const FewParams& p, bool early, cudaStream_t st) {
+  // the depth over the warps: four chunks of 32 each where there is as much
+  int warps = p.K / 128;
+  warps = warps < 2 ? 2 : warps > (DUAL ? 8 : 16) ? (DUAL ? 8 : 16) : warps;
+  const size_t smem = sizeof(float) * warps * (DUAL ? 2 : 1) * NT * 128;
+  return launch_pdl(early, k_ffn_few<F32, NT, DUAL>, dim3(static_cast<unsigned>((p.rows + 15) / 16)),
+                    dim3(static_cast<unsigned>(warps * 32)), smem, st, p);
+}
+
+template <bool F32, bool DUAL>
+static cudaError_t run_few(const FewParams& p, bool early, cudaStream_t st) {
+  return p.T <= 8    ? run_few<F32, 1, DUAL>(p, early, st)
+         : p.T <= 16 ? run_few<F32, 2, DUAL>(p, early, st)
+                     : run_few<F32, 4, DUAL>(p, early, st);
+}
+
+template <bool F32>
+static cudaError_t forward_few(const FfnArgs& a) {
+  using TT = typename std::conditional<F32, float, bf16>::type;
+  const Layout l = layout(a, false);
+  const int T = static_cast<int>(a.B * a.L), C = static_cast<int>(a.C), F = static_cast<int>(a.F);
+  bf16* hid = reinterpret_cast<bf16*>(static_cast<char*>(a.ws) + l.hid);
+  const bf16* x = static_cast<const bf16*>(a.x);
+  if (!l.token || F32) {
+    bf16* to = reinterpret_cast<bf16*>(static_cast<char*>(a.ws) + l.x);
+    k_ffn_gather<TT><<<static_cast<unsigned>(cdiv(static_cast<long long>(T) * C, 256)), 256, 0, a.stream>>>(
+        static_cast<const TT*>(a.x), to, C, static_cast<int>(a.L), T, l.act_plane);
+    x = to;
+  }
+  FewParams h{};
+  h.w0 = a.wg, h.w1 = a.wu, h.x = x, h.x_plane = l.act_plane;
+  h.T = T, h.rows = F, h.K = C, h.act = a.act;
+  h.hid = hid, h.hid_plane = l.hid_plane;
+  cudaError_t e = run_few<F32, true>(h, false, a.stream);
+  if (e != cudaSuccess) return e;
+  FewParams y{};
+  y.w0 = a.wd, y.x = hid, y.x_plane = l.hid_plane;
+  y.T = T, y.rows = C, y.K = F;
+  y.y = a.y, y.L = static_cast<int>(a.L);
+  return run_few<F32, false>(y, true, a.stream);
 }
 
 template <bool F32>
@@ -415,6 +487,7 @@ struct Ffn {
 };
 
 cudaError_t launch_ffn_forward(const FfnArgs& a) {
+  if (a.B * a.L <= kFewMost) return a.bf16 ? forward_few<false>(a) : forward_few<true>(a);
   return a.bf16 ? Ffn<false>(a, false).forward() : Ffn<true>(a, false).forward();
 }
 

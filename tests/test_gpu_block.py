@@ -405,6 +405,14 @@ FFN = [
     ((1,), 4, 256, 520, "bf16", "silu"),          # single tokens
     ((1,), 7, 264, 136, "f32", "silu"),
     ((1,), 16, 128, 512, "bf16", "gelu"),
+    ((1,), 8, 2048, 40, "bf16", "silu"),
+    ((1,), 9, 40, 2048, "f32", "gelu"),
+    ((1,), 32, 264, 328, "bf16", "silu"),
+    ((1,), 33, 264, 328, "bf16", "silu"),
+    ((1,), 25, 72, 136, "f32", "silu"),
+    ((2, 3), 4, 72, 104, "bf16", "gelu"),         # a few positions of short samples
+    ((5,), 3, 136, 72, "f32", "silu"),
+    ((32,), 1, 64, 96, "bf16", "silu"),
     ((1,), 17, 128, 512, "bf16", "gelu"),
     ((1,), 200, 72, 200, "bf16", "silu"),         # token-major
     ((1,), 130, 64, 264, "f32", "gelu"),

@@ -10,18 +10,20 @@
 // is the contiguous axis of D (positions of [B, C, L] outputs, channels of a
 // weight gradient) a warp's stores of one n are adjacent; the hidden
 // activations, which only these products read, lie the other way, [position]
-// [channel], so that a thread stores its 16 adjacent channels in one
-// instruction.
+// [channel], so that a thread has neighbouring channels to pack and store.
 //
 // A pair of CTAs computes a 256 x 256 tile (cta_group::2): each holds 128 rows
 // of A, half of B's columns and 128 accumulator lanes.  One warp issues TMA,
 // one (of the leading CTA) the MMAs, eight read the accumulators back.
 // Accumulators are fp32 in tensor memory, two of 256 columns, so that the
-// epilogue of a tile runs under the products of the next.  Where the epilogue
-// needs G, U and dH together a tile has 80 hidden channels: 80 + 80 + 96
-// columns (the pair's MMA wants a multiple of 32) fill one of the two
-// accumulators.  One accumulator of three times 128, and no overlap, took 106
-// instead of the present time at C 256, F 1024 and 32768 positions.
+// epilogue of a tile runs under the products of the next.  An MMA of the pair
+// takes about 128 cycles for 256 columns and hardly fewer for fewer, so every
+// product has 256 where it can: G and U of 128 hidden channels side by side,
+// and where the epilogue needs dH too, dH of 256 hidden channels in one half of
+// tensor memory while their G and U pass through the other in two turns.
+// (Tiles of 80 channels, 80 + 80 + 96 columns in each of two accumulators,
+// overlap the epilogue but took 74 us where this takes 51, at C 256, F 1024
+// and 32768 positions.)
 //
 // fp32 operands come as three bf16 planes (high, middle, low: 24 bits) and
 // every K loop runs over the six plane products that reach 2^-24, the small
@@ -43,11 +45,9 @@
 namespace hnd {
 namespace ffn {
 
-constexpr int kThreads = 352;          // a warp for A's copies, one for the MMAs, 8 of epilogue, one for B's copies
 constexpr int kBK = 64;                // depth of a stage
 constexpr int kHalf = 128 * kBK * 2;   // bytes of A (and of B) per CTA and stage
 constexpr int kStage = 2 * kHalf;
-constexpr int kStoreBytes = 32 * 128 * 2;   // one TMA store: 32 rows n of 128 m
 
 // One stretch of a K loop.
 struct Seg {
@@ -55,7 +55,7 @@ struct Seg {
   int a_mn, b_mn;            // 1: the tile's m (n) axis is contiguous in memory
   int a_batched, b_batched;  // the map's third coordinate follows the batch
   int ncols;                 // columns over the pair, at most 256
-  int nstep, noff;           // n of a tile, and of the second CTA's part in it
+  int nstep, noff, nbase;    // n from tile to tile, to the second CTA's part, and of the tile's first
   int acc;                   // first accumulator column
   int clear;                 // starts this accumulator
 };
@@ -83,7 +83,7 @@ struct Job {
   long long group, gs;       //   (m / group) gs + n rs + m % group; kOutTok: m rs + n
 };
 
-constexpr int kMaxMaps = 10, kMaxSegs = 4, kMaxJobs = 3;
+constexpr int kMaxMaps = 10, kMaxSegs = 3, kMaxJobs = 3;
 
 struct Params {
   CUtensorMap map[kMaxMaps];
@@ -95,7 +95,8 @@ struct Params {
   int act;
   // the hidden tensors [plane][batch][position][channel]
   __nv_bfloat16* hid[3];
-  long long hid_plane, hid_bs, hid_rs;
+  long long hid_plane, hid_rs;
+  int hmap[3];               // bf16: their maps
   int* status;
 };
 
@@ -262,6 +263,26 @@ __device__ __forceinline__ float recip_fast(float x) {
   return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair64(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float (&o)[2]) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o[0]), "=f"(o[1]) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 1 / (1 + exp(-g)) of two gates.  bf16: one reciprocal of the product serves
 // both, since the special-function unit (two exponentials and two reciprocals
 // for a pair otherwise) is what the epilogue waits for; exp(-g) is held at
@@ -273,7 +294,9 @@ __device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
     s[0] = recip_fast(1.f + expf(fminf(-g[0], 87.f)));     // off by one unit in the last place at most
     s[1] = recip_fast(1.f + expf(fminf(-g[1], 87.f)));
   } else {
-    const float d0 = 1.f + exp2_fast(fminf(-kLog2e * g[0], 60.f)), d1 = 1.f + exp2_fast(fminf(-kLog2e * g[1], 60.f));
+    float x[2];
+    unpair(mul2(pair64(g[0], g[1]), pair64(-kLog2e, -kLog2e)), x);
+    const float d0 = 1.f + exp2_fast(fminf(x[0], 60.f)), d1 = 1.f + exp2_fast(fminf(x[1], 60.f));
     const float r = recip_fast(d0 * d1);
     s[0] = r * d1;
     s[1] = r * d0;
@@ -284,9 +307,13 @@ __device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
 template <bool F32, int ACT>
 __device__ __forceinline__ void hidden2(const float (&g)[2], const float (&u)[2], float (&h)[2]) {
   float s[2];
-  if constexpr (ACT == 0) sigmoid2<F32>(g, s);
+  if constexpr (ACT == 0) {
+    sigmoid2<F32>(g, s);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) h[i] = g[i] * (ACT ? 0.5f + 0.5f * erff(g[i] * kSqrtHalf) : s[i]) * u[i];
+    for (int i = 0; i < 2; ++i) s[i] = 0.5f + 0.5f * erff(g[i] * kSqrtHalf);
+  }
+  unpair(mul2(mul2(pair64(g[0], g[1]), pair64(s[0], s[1])), pair64(u[0], u[1])), h);
 }
 
 // H, dG and dU of two hidden channels.
@@ -304,7 +331,7 @@ __device__ __forceinline__ void hidden_grads2(const float (&g)[2], const float (
       da = cdf + g[i] * kInvSqrt2Pi * (F32 ? expf(-0.5f * g[i] * g[i]) : exp2_fast(-0.5f * kLog2e * g[i] * g[i]));
     } else {
       a = g[i] * s[i];
-      da = s[i] + a * (1.f - s[i]);
+      da = fmaf(a, 1.f - s[i], s[i]);
     }
     h[i] = a * u[i];
     dg[i] = d[i] * u[i] * da;
@@ -345,16 +372,6 @@ __device__ __forceinline__ void with_act(int act, Fn fn) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 32 bytes in one store.
-struct alignas(32) Vec32 {
-  uint32_t w[8];
-};
-__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(HND_G(reinterpret_cast<Vec32*>(p))),
-               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
 }
 
 __device__ __forceinline__ void stage_put(uint32_t addr, float v) {
@@ -437,26 +454,35 @@ __device__ __forceinline__ void planes_of(int combo, int& a, int& b) {
 
 template <int EPI, bool F32>
 struct Plan {
-  static constexpr int kBufs = 2;                                   // accumulators of 256 columns
+  static constexpr int kTurns = EPI == kEpiGrad && !F32 ? 2 : 1;    // of G and U in a tile
+  static constexpr int kSegs = kTurns + 1;                          // segments of a job at most
+  static constexpr int kBufs = kTurns == 2 ? 1 : 2;                 // accumulators of 256 columns
   static constexpr int kPiece = F32 ? 2 : 1 << 30;                  // stages added up in tensor memory
   // columns of a tile: hidden channels, or columns of D.  fp32 has fewer: a
-  // thread holds its columns' sums in registers, 64 to 96 of the 168 it has
-  static constexpr int kCols = EPI == kEpiOut ? (F32 ? 128 : 256) : F32 ? 64 : EPI == kEpiGrad ? 80 : 128;
-  static constexpr int kGradCols = F32 ? 64 : 96;                   // columns of dH
-  static constexpr int kStages = EPI == kEpiOut ? 6 : 7;
+  // thread holds its columns' sums in registers
+  static constexpr int kCols = F32 ? (EPI == kEpiOut ? 128 : 64) : EPI == kEpiHidden ? 128 : 256;
   static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;
-  static constexpr int kStoreBufs = 2;                              // of each half of the epilogue (kEpiOut)
-  static constexpr int kStore = EPI == kEpiOut ? 2 * kStoreBufs * kStoreBytes : 0;
-  static constexpr int kSmem = 1024 + kStages * kStage + kStore + 8 * (2 * kStages + 2 * kBufs) + 16;
+  // Four warps of epilogue see all lanes; two such groups share the columns.
+  static constexpr int kGroups = 2;
+  static constexpr int kThreads = 32 * (3 + 4 * kGroups);           // a warp for A's copies, one for the MMAs, one for B's
+  // bf16 leaves by TMA, gathered in shared memory: of each group and output
+  // 128 positions x kWide hidden channels, or (kEpiOut) 32 n x 128 m; twice,
+  // so that a copy out runs under the next one's gathering
+  static constexpr int kWide = EPI == kEpiGrad ? 32 : 64;
+  static constexpr int kStoreBytes = EPI == kEpiOut ? 8192 : 256 * kWide;
+  static constexpr int kGroupStore = F32 ? 0 : 2 * kOuts * kStoreBytes;
+  static constexpr int kStages = F32 ? 7 : EPI == kEpiGrad ? 4 : EPI == kEpiHidden ? 5 : 6;
+  static constexpr int kSmem = 1024 + kStages * kStage + kGroups * kGroupStore + 8 * (2 * kStages + 2 * kBufs) + 16;
 };
 
 template <int EPI, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_gemm(const __grid_constant__ Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThreads, 1)
+    k_ffn_gemm(const __grid_constant__ Params p) {
   using PL = Plan<EPI, F32>;
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
   const uint32_t base = (s32(hnd_dyn_smem) + 1023) & ~1023u;
   const uint32_t out = base + PL::kStages * kStage;
-  const uint32_t bars = out + PL::kStore;
+  const uint32_t bars = out + PL::kGroups * PL::kGroupStore;
   const uint32_t full = bars, empty = full + 8 * PL::kStages, accf = empty + 8 * PL::kStages,
                  acce = accf + 8 * PL::kBufs, tmem_slot = acce + 8 * PL::kBufs;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -466,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < PL::kStages; ++i) bar_init(full + 8 * i, 1), bar_init(empty + 8 * i, 1);
-    for (int i = 0; i < PL::kBufs; ++i) bar_init(accf + 8 * i, 1), bar_init(acce + 8 * i, 16);
+    for (int i = 0; i < PL::kBufs; ++i) bar_init(accf + 8 * i, 1), bar_init(acce + 8 * i, 8 * PL::kGroups);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
@@ -482,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
 
   bool ok = true;
-  if (warp == 0 || warp == kThreads / 32 - 1) {
+  if (warp == 0 || warp == PL::kThreads / 32 - 1) {
     // ---- TMA: this CTA's 128 rows of A (first warp) and its part of B (last
     // warp).  A warp goes through the loop as one and a single lane issues:
     // under a branch on the lane every operand of a copy would first have to
@@ -491,9 +517,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
     int st = 0, ph = 0;
     const uint32_t lead_full = in_leader(full);
     Walk walk;
-    int job = -1, nseg = 0, kblocks = 0, mn[2], half_n[2], step[2], off[2], batched[2];
-    uint32_t bytes[2];
-    const CUtensorMap* map[2];
+    constexpr int S = PL::kSegs;
+    int job = -1, nseg = 0, kblocks = 0, wide = 0, mn[S], half_n[S], step[S], off[S], batched[S];
+    uint32_t bytes[S];
+    const CUtensorMap* map[S];
     bool long_k = false;
     for (int t = pair; ok && t < p.tiles; t += pairs) {
       walk.seek(p, t);
@@ -503,13 +530,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
         nseg = pinned(j.nseg);
         kblocks = pinned(j.kblocks);
         long_k = pinned(j.kbatches) > 1;
+        wide = pinned(static_cast<int>(j.N));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S; ++i) {
           const Seg& s = p.seg[j.seg0 + (i < nseg ? i : 0)];
           mn[i] = pinned(is_b ? s.b_mn : s.a_mn);
           half_n[i] = pinned(is_b ? s.ncols / 2 : 128);
           step[i] = pinned(is_b ? s.nstep : 256);
-          off[i] = pinned(static_cast<int>(rank) * (is_b ? s.noff : 128));
+          off[i] = pinned(static_cast<int>(rank) * (is_b ? s.noff : 128) + (is_b ? s.nbase : 0));
           batched[i] = pinned(is_b ? s.b_batched : s.a_batched);
           // MN-major boxes are 64 wide, also where fewer are used
           bytes[i] = pinned(2 * (kHalf + 2 * kBK * (s.b_mn && s.ncols < 128 ? 64 : s.ncols / 2)));
@@ -529,8 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
         }
         const int from = F32 ? lo + pc / combos * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i >= nseg) continue;
+        for (int i = 0; i < S; ++i) {
+          if (i >= nseg || (i == 2 && ti.nt * 256 + 128 >= wide)) continue;      // no second turn behind the last channel
           const int r0 = (is_b ? ti.nt : ti.mt) * step[i] + off[i];
           int bat = long_k ? from / kblocks : ti.batch, k = (long_k ? from - bat * kblocks : from) * kBK;
           for (int kb = from; ok && kb < to; ++kb) {
@@ -563,8 +591,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
     // ---- MMA: one lane of the leading CTA's warp
     const bool lead = elected();
     if (rank == 0) {
-      int st = 0, ph = 0, buf = 0, bph = 0, job = -1, nseg = 0, a_mn[2], b_mn[2], acc[2], clear[2];
-      uint32_t id[2];
+      constexpr int S = PL::kSegs;
+      int st = 0, ph = 0, buf = 0, bph = 0, job = -1, nseg = 0, wide = 0, a_mn[S], b_mn[S], acc[S], clear[S];
+      uint32_t id[S];
       Walk walk;
       for (int t = pair; ok && t < p.tiles; t += pairs) {
         walk.seek(p, t);
@@ -572,8 +601,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
           job = walk.job;
           const Job& j = p.job[job];
           nseg = pinned(j.nseg);
+          wide = pinned(static_cast<int>(j.N));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < S; ++i) {
             const Seg& s = p.seg[j.seg0 + (i < nseg ? i : 0)];
             a_mn[i] = pinned(s.a_mn), b_mn[i] = pinned(s.b_mn);
             acc[i] = pinned(s.acc), clear[i] = pinned(s.clear);
@@ -582,15 +612,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
         }
         int lo, hi;
         walk.range(walk.split(t), lo, hi);
-        const int pieces = pieces_of<PL::kPiece>(lo, hi);
+        // what is handed to the epilogue at a time: a piece of fp32's sums, or a turn of G and U
+        int pieces = pieces_of<PL::kPiece>(lo, hi);
+        if (PL::kTurns == 2) pieces = walk.tile(t).nt * 256 + 128 < wide ? 2 : 1;
         for (int pc = 0; ok && pc < pieces; ++pc) {
           if (!(ok = warp_wait(acce + 8 * buf, bph ^ 1, p.status))) break;
           tmem_fence_after();
           const int from = F32 ? lo + pc * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
           for (int c = 0; ok && c < combos; ++c)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (i >= nseg) continue;
+            for (int i = 0; i < S; ++i) {
+              if (i >= nseg || (PL::kTurns == 2 && (i == 2) != (pc == 1))) continue;
               const uint32_t d = tmem + buf * 256 + acc[i];
               const uint32_t da = a_mn[i] ? 2048 >> 4 : 32 >> 4, db = b_mn[i] ? 2048 >> 4 : 32 >> 4;
               bool add = c > 0 || !clear[i];
@@ -616,15 +648,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
       }
     }
   } else {
-    // ---- epilogue: two halves of four warps, each half takes half the columns
-    const int quad = warp % 4, half = (warp - 2) / 4, row = quad * 32 + lane;
+    // ---- epilogue: groups of four warps, each takes its part of the columns
+    constexpr int GR = PL::kGroups;
+    const int quad = warp % 4, group = (warp - 2) / 4, row = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const bool issuer = (warp == 2 || warp == 6) && lane == 0;
-    const uint32_t stage = out + half * (PL::kStoreBufs * kStoreBytes);
-    int buf = 0, bph = 0, sbuf = 0, turn = half;
-    // all four warps of the half go on, or none: they meet at barriers below
+    const bool issuer = (warp - 2) % 4 == 0 && lane == 0;
+    const uint32_t stage = out + group * PL::kGroupStore;
+    int buf = 0, bph = 0, sbuf = 0;
+    // all four warps of the group go on, or none: they meet at barriers below
     auto arrived = [&] {
-      const bool yes = named_all(1 + half, 128, bar_wait(accf + 8 * buf, bph, p.status));
+      const bool yes = named_all(1 + group, 128, bar_wait(accf + 8 * buf, bph, p.status));
       tmem_fence_after();
       return yes;
     };
@@ -643,9 +676,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
       const long long m = m0 + row;
       const bool live = m < j.M;
       if constexpr (F32) {
-        // sum[q][i]: product q of the tile at this half's column i
+        // sum[q][i]: product q of the tile at this group's column i
         constexpr int Q = EPI == kEpiOut ? 1 : EPI == kEpiHidden ? 2 : 3;
-        constexpr int W = PL::kCols / 2;
+        constexpr int W = PL::kCols / GR;
         float sum[Q][W];
         int lo, hi;
         walk.range(ti.split, lo, hi);
@@ -653,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
         bool yes = true;
         for (int pc = 0; pc < pieces; ++pc) {
           if (!(yes = arrived())) break;
-          const uint32_t acc = tmem + lanes + buf * 256 + half * W;
+          const uint32_t acc = tmem + lanes + buf * 256 + group * W;
 #pragma unroll
           for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -668,7 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
           release();
         }
         if (!yes) break;
-        const int n0 = ti.nt * PL::kCols + half * W;
+        const int n0 = ti.nt * PL::kCols + group * W;
         if constexpr (EPI == kEpiOut) {
           if (j.kind == kOutF32) {
             const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
@@ -720,27 +753,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
             }
         }
       } else {
-        if (!arrived()) break;
-        const uint32_t acc = tmem + lanes + buf * 256;
         if constexpr (EPI == kEpiOut) {
+          if (!arrived()) break;
+          const uint32_t acc = tmem + lanes + buf * 256 + group * 128;
           const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
           for (int c0 = 0; c0 < 128; c0 += 32) {
-            const int n0 = ti.nt * 256 + half * 128 + c0;
+            const int n0 = ti.nt * 256 + group * 128 + c0;
             uint32_t v[32];
-            tmem_load(v, acc + half * 128 + c0);
+            tmem_load(v, acc + c0);
             tmem_wait_load();
             if (c0 == 96) release();
             if (j.kind == kOutTma) {
-              const uint32_t sb = stage + sbuf * kStoreBytes;
-              if (issuer) store_wait_read<PL::kStoreBufs - 1>();
-              named_sync(1 + half, 128);
+              const uint32_t sb = stage + sbuf * PL::kStoreBytes;
+              if (issuer) store_wait_read<1>();
+              named_sync(1 + group, 128);
 #pragma unroll
               for (int i = 0; i < 32; ++i) stage_put(sb + i * 256 + row * 2, __uint_as_float(v[i]));
               fence_async();
-              named_sync(1 + half, 128);
+              named_sync(1 + group, 128);
               if (issuer && m0 < j.M && n0 < j.N) tma_store(&p.map[j.map], sb, m0, n0, ti.batch);
               if (issuer) store_commit();
-              sbuf = (sbuf + 1) % PL::kStoreBufs;
+              sbuf ^= 1;
             } else if (j.kind == kOutBf16) {
               __nv_bfloat16* o = static_cast<__nv_bfloat16*>(j.ptr) + at;
 #pragma unroll
@@ -765,49 +798,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_g
             }
           }
         } else {
-          // the tile's hidden channels in pieces of W, taken by the two halves in turn (of 5 pieces each half
-          // takes 3 in every second tile)
-          constexpr int W = EPI == kEpiGrad ? 16 : 32, kPieces = PL::kCols / W;
-          __nv_bfloat16* o = p.hid[0] + ti.batch * p.hid_bs + m * p.hid_rs + ti.nt * PL::kCols;
-          const long long apart[3] = {0, p.hid[1] - p.hid[0], p.hid[2] - p.hid[0]};
-          const int left = static_cast<int>(j.N) - ti.nt * PL::kCols;      // channels of the tile that exist
-          for (int k = turn; k < kPieces; k += 2) {
-            uint32_t g[W], u[W], d[EPI == kEpiGrad ? W : 1];
-            tmem_load(g, acc + k * W);
-            tmem_load(u, acc + PL::kCols + k * W);
-            if constexpr (EPI == kEpiGrad) tmem_load(d, acc + 2 * PL::kCols + k * W);
-            tmem_wait_load();
-            if (k + 2 >= kPieces) release();
+          // a turn's 128 hidden channels: 64 of each group, 16 at a time, gathered as rows of kWide channels of a
+          // position (a thread's own 32-byte stores leave an SM at 16 bytes a cycle: 90 us for the gradients at C
+          // 256, F 1024, 32768 positions)
+          constexpr int W = 16, kPer = PL::kWide / W, kChunks = PL::kWide / 8;
+          bool yes = true;
+          for (int turn = 0; turn < PL::kTurns; ++turn) {
+            const int n0 = ti.nt * PL::kCols + turn * 128;
+            if (n0 >= j.N || !(yes = arrived())) break;
+            const uint32_t acc = tmem + lanes + buf * 256 + group * 64;
+            // the next 16 channels are on their way while these are worked on
+            uint32_t g[2][W], u[2][W], d[2][EPI == kEpiGrad ? W : 1];
+            auto load = [&](int c) {
+              tmem_load(g[c & 1], acc + c * W);
+              tmem_load(u[c & 1], acc + 128 + c * W);
+              if constexpr (EPI == kEpiGrad) tmem_load(d[c & 1], acc + 256 + turn * 128 + c * W);
+            };
+            load(0);
             with_act(p.act, [&](auto kind) {
               constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-              for (int i0 = 0; i0 < W; i0 += 16) {
+              for (int c = 0; c < 64 / W; ++c) {
+                tmem_wait_load();
+                if (c + 1 < 64 / W)
+                  load(c + 1);
+                else
+                  release();
+                const uint32_t to = stage + sbuf * (PL::kOuts * PL::kStoreBytes);
+                if (c % kPer == 0) {      // this buffer's copies before the last have left it
+                  if (issuer) store_wait_read<1>();
+                  named_sync(1 + group, 128);
+                }
                 uint32_t w[PL::kOuts][8];
 #pragma unroll
-                for (int i = i0; i < i0 + 16; i += 2) {
-                  const float gv[2] = {__uint_as_float(g[i]), __uint_as_float(g[i + 1])};
-                  const float uv[2] = {__uint_as_float(u[i]), __uint_as_float(u[i + 1])};
+                for (int i = 0; i < W; i += 2) {
+                  const float gv[2] = {__uint_as_float(g[c & 1][i]), __uint_as_float(g[c & 1][i + 1])};
+                  const float uv[2] = {__uint_as_float(u[c & 1][i]), __uint_as_float(u[c & 1][i + 1])};
                   float r[3][2];
                   if constexpr (EPI == kEpiGrad) {
-                    const float dv[2] = {__uint_as_float(d[i]), __uint_as_float(d[i + 1])};
+                    const float dv[2] = {__uint_as_float(d[c & 1][i]), __uint_as_float(d[c & 1][i + 1])};
                     hidden_grads2<false, ACT>(gv, uv, dv, r[0], r[1], r[2]);
                   } else {
                     hidden2<false, ACT>(gv, uv, r[0]);
                   }
 #pragma unroll
-                  for (int q = 0; q < PL::kOuts; ++q) w[q][(i - i0) / 2] = pack2(r[q][0], r[q][1]);
+                  for (int q = 0; q < PL::kOuts; ++q) w[q][i / 2] = pack2(r[q][0], r[q][1]);
                 }
-                if (live && k * W + i0 < left)
+                // 16-byte chunks of the row, under the 64- or 128-byte swizzle
+                const int key = kChunks == 8 ? row & 7 : row >> 1 & 3;
 #pragma unroll
-                  for (int q = 0; q < PL::kOuts; ++q) store32(o + apart[q] + k * W + i0, w[q]);
+                for (int q = 0; q < PL::kOuts; ++q)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + q * PL::kStoreBytes + row * (2 * PL::kWide) +
+                                     (((c % kPer * 2 + i) ^ key) << 4)),
+                                 "r"(w[q][4 * i]), "r"(w[q][4 * i + 1]), "r"(w[q][4 * i + 2]), "r"(w[q][4 * i + 3])
+                                 : "memory");
+                if (c % kPer == kPer - 1) {
+                  fence_async();
+                  named_sync(1 + group, 128);
+                  if (issuer) {
+                    const int n = n0 + group * 64 + c / kPer * PL::kWide;
+                    if (m0 < j.M && n < j.N)
+#pragma unroll
+                      for (int q = 0; q < PL::kOuts; ++q)
+                        tma_store(&p.map[p.hmap[q]], to + q * PL::kStoreBytes, n, m0, ti.batch);
+                    store_commit();
+                  }
+                  sbuf ^= 1;
+                }
               }
             });
           }
-          if (kPieces % 2) turn ^= 1;
+          if (!yes) break;
         }
       }
     }
-    if (EPI == kEpiOut && issuer) store_wait_read<0>();
+    if (!F32 && issuer) store_wait_read<0>();
   }
   __syncwarp();
   tmem_fence_before();

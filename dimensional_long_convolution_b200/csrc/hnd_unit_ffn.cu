@@ -124,7 +124,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   l.batches = merged ? 1 : a.B;
   l.Lx = merged ? T : a.L;
   l.pitch = l.token ? a.C : up(T, 8);
-  l.hpitch = up(a.F, 16);      // whole 32-byte stores
+  l.hpitch = a.F;
   const bool copied = l.packed || !a.bf16;
   size_t at = 0;
   auto take = [&](long long elements, size_t size) {
@@ -184,7 +184,7 @@ struct Mat {
   long long inner, rows, count, pitch, batch;
 };
 
-static bool encode(CUtensorMap* map, const Mat& m, int box_inner, int box_rows, bool swizzled) {
+static bool encode(CUtensorMap* map, const Mat& m, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
   const EncodeFn fn = encoder();
   if (!fn) return false;
   const cuuint64_t dim[3] = {static_cast<cuuint64_t>(m.inner), static_cast<cuuint64_t>(m.rows),
@@ -193,8 +193,7 @@ static bool encode(CUtensorMap* map, const Mat& m, int box_inner, int box_rows, 
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(m.p), dim, stride, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // -------------------------------------------------------------------- launch
@@ -203,17 +202,21 @@ struct Launch {
   int maps = 0, segs = 0;
   bool ok = true;
 
-  int add(const Mat& m, int box_inner, int box_rows, bool swizzled) {
-    if (maps == kMaxMaps || !encode(&p.map[maps], m, box_inner, box_rows, swizzled)) {
+  int add(const Mat& m, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
+    if (maps == kMaxMaps || !encode(&p.map[maps], m, box_inner, box_rows, swizzle)) {
       ok = false;
       return 0;
     }
     return maps++;
   }
   // an operand whose tile axis (m or n) is contiguous / whose k axis is
-  int mn(const Mat& m) { return add(m, 64, kBK, true); }
-  int km(const Mat& m, int rows = 128) { return add(m, kBK, rows, true); }
-  int store(const Mat& m) { return add(m, 128, 32, false); }
+  int mn(const Mat& m) { return add(m, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B); }
+  int km(const Mat& m, int rows = 128) { return add(m, kBK, rows, CU_TENSOR_MAP_SWIZZLE_128B); }
+  int store(const Mat& m) { return add(m, 128, 32, CU_TENSOR_MAP_SWIZZLE_NONE); }
+  // hidden rows of `wide` channels
+  int store_hidden(const Mat& m, int wide) {
+    return add(m, wide, 128, wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   void job(const Job& j) { p.job[p.jobs++] = j; }
 };
 
@@ -238,7 +241,7 @@ static cudaError_t run(Launch& l, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   long long pairs = sm_count() / 2;
   if (pairs > tiles) pairs = tiles;
-  kern<<<static_cast<unsigned>(2 * pairs), kThreads, smem, st>>>(l.p);
+  kern<<<static_cast<unsigned>(2 * pairs), Plan<EPI, F32>::kThreads, smem, st>>>(l.p);
   return cudaGetLastError();
 }
 
@@ -352,13 +355,13 @@ struct Ffn {
   // is contiguous, except token-major, where the channels are
   int positions(Launch& n, const Mat& m) const { return l.token ? n.km(m) : n.mn(m); }
   Seg data_seg(int ma, int mb, bool a_mn, bool b_mn, int ncols, int acc, int clear) const {
-    return Seg{ma, mb, mb, a_mn, b_mn, l.batches > 1, 0, ncols, ncols, ncols / 2, acc, clear};
+    return Seg{ma, mb, mb, a_mn, b_mn, l.batches > 1, 0, ncols, ncols, ncols / 2, 0, acc, clear};
   }
   // G and U of `cols` hidden channels side by side: the first CTA brings Wg, the second Wu
-  Seg gates_seg(Launch& n, int cols) const {
+  Seg gates_seg(Launch& n, int cols, int step) const {
     Seg s = data_seg(positions(n, x), n.km(wg, cols), !l.token, false, 2 * cols, 0, 1);
     s.b1 = n.km(wu, cols);
-    s.nstep = cols;
+    s.nstep = step;
     s.noff = 0;
     return s;
   }
@@ -375,9 +378,11 @@ struct Ffn {
     return j;
   }
   void hidden_out(Launch& n, int count) const {
-    for (int i = 0; i < count; ++i) n.p.hid[i] = static_cast<bf16*>(const_cast<void*>(hid[i].p));
+    for (int i = 0; i < count; ++i) {
+      n.p.hid[i] = static_cast<bf16*>(const_cast<void*>(hid[i].p));
+      if (!F32) n.p.hmap[i] = n.store_hidden(hid[i], count == 1 ? Plan<kEpiHidden, F32>::kWide : PG::kWide);
+    }
     n.p.hid_plane = l.hid_plane;
-    n.p.hid_bs = l.Lx * l.hpitch;
     n.p.hid_rs = l.hpitch;
   }
   // y or dx: back to the activations' own layout
@@ -401,7 +406,7 @@ struct Ffn {
     cudaError_t e;
     if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_weights()) != cudaSuccess) return e;
     Launch h = start();
-    h.p.seg[0] = gates_seg(h, hn);
+    h.p.seg[0] = gates_seg(h, hn, hn);
     hidden_out(h, 1);
     h.job(data_job(1, a.F, hn, a.C));
     if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
@@ -420,11 +425,16 @@ struct Ffn {
       return e;
     // H, dG, dU
     Launch h = start();
-        h.p.seg[0] = gates_seg(h, gn);
-    h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, PG::kGradCols, 2 * gn, 1);
-    h.p.seg[1].nstep = gn;
+        if (F32) {
+      h.p.seg[0] = gates_seg(h, gn, gn);
+      h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, gn, 2 * gn, 1);
+    } else {      // dH of 256 channels, then G and U of 128 and of the other 128
+      h.p.seg[0] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, gn, 256, 1);
+      h.p.seg[1] = h.p.seg[2] = gates_seg(h, 128, gn);
+      h.p.seg[2].nbase = 128;
+    }
     hidden_out(h, 3);
-    h.job(data_job(2, a.F, gn, a.C));
+    h.job(data_job(F32 ? 2 : 3, a.F, gn, a.C));
     if ((e = run<kEpiGrad, F32>(h, a.stream)) != cudaSuccess) return e;
     // dX
     Launch d = start();
@@ -441,7 +451,7 @@ struct Ffn {
     const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, on / 2);
     const int mh = w.mn(hid[0]), mdg = w.mn(hid[1]), mdu = w.mn(hid[2]);
     auto seg = [&](int ma, int mb, int a_mn, int b_mn) {
-      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 1};
+      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 0, 1};
     };
     w.p.seg[0] = seg(mx, mdg, l.token, 1);
     w.p.seg[1] = seg(mx, mdu, l.token, 1);

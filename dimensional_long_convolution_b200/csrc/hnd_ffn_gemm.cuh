@@ -506,6 +506,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
   tmem_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  // so far under the kernel in front; the next one may set itself up too
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   bool ok = true;
   if (warp == 0 || warp == PL::kThreads / 32 - 1) {

@@ -17,21 +17,31 @@ using namespace ffn;
 // [B, C, L] -> rows c of B L adjacent positions at `pitch`: bf16 as it is,
 // fp32 as three bf16 planes.  Used where samples are too short or too ragged
 // for TMA, and for every fp32 operand (weights and token-major activations
-// are B = 1).
+// are B = 1).  All operands of a call in one launch, blockIdx.y each.
+struct Pack {
+  const void* x;
+  bf16* out;
+  long long C, L, T, pitch, plane;
+};
+constexpr int kMaxPacks = 5;
+struct Packs {
+  Pack p[kMaxPacks];
+};
+
 template <class TT>
-__global__ void __launch_bounds__(256)
-    k_ffn_pack(const TT* __restrict__ x, bf16* __restrict__ out, long long C, long long L, long long T, long long pitch,
-               long long plane) {
-  const long long groups = pitch / 8, n = groups * C;
+__global__ void __launch_bounds__(256) k_ffn_pack(const Packs packs) {
+  const Pack& p = packs.p[blockIdx.y];
+  const TT* x = static_cast<const TT*>(p.x);
+  const long long groups = p.pitch / 8, n = groups * p.C;
   for (long long g = blockIdx.x * 256LL + threadIdx.x; g < n; g += gridDim.x * 256LL) {
-    const long long c = g / groups, t0 = g % groups * 8;
-    long long b = t0 / L, l = t0 % L;
+    const long long c = g / groups, t0 = (g - c * groups) * 8;
+    long long b = t0 / p.L, l = t0 - b * p.L;
     __align__(16) bf16 v[3][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float f = 0.f;
-      if (t0 + i < T) f = ld1(x + (b * C + c) * L + l);
-      if (++l == L) l = 0, ++b;
+      if (t0 + i < p.T) f = ld1(x + (b * p.C + c) * p.L + l);
+      if (++l == p.L) l = 0, ++b;
       if (sizeof(TT) == 4)
         split3(f, v[0][i], v[1][i], v[2][i]);
       else
@@ -39,7 +49,7 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int k = 0; k < (sizeof(TT) == 4 ? 3 : 1); ++k)
-      *HND_G(reinterpret_cast<uint4*>(out + k * plane + c * pitch + t0)) = *reinterpret_cast<const uint4*>(v[k]);
+      *HND_G(reinterpret_cast<uint4*>(p.out + k * p.plane + c * p.pitch + t0)) = *reinterpret_cast<const uint4*>(v[k]);
   }
 }
 
@@ -61,10 +71,16 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The sum of a weight gradient's partial products, in the order of the splits.
+// The sums of the weight gradients' partial products, in the order of the
+// splits; blockIdx.y: which gradient.
+struct Sums {
+  void* out[3];
+};
+
 template <class TT>
-__global__ void __launch_bounds__(256)
-    k_ffn_sum(const float* __restrict__ part, TT* __restrict__ out, long long n, int splits) {
+__global__ void __launch_bounds__(256) k_ffn_sum(const float* __restrict__ parts, const Sums sums, long long n, int splits) {
+  const float* part = parts + blockIdx.y * (n * splits);
+  TT* out = static_cast<TT*>(sums.out[blockIdx.y]);
   for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 4; i < n; i += gridDim.x * 1024LL) {
     float4 s = *HND_G(reinterpret_cast<const float4*>(part + i));
     for (int k = 1; k < splits; ++k) {
@@ -241,8 +257,7 @@ static cudaError_t run(Launch& l, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   long long pairs = sm_count() / 2;
   if (pairs > tiles) pairs = tiles;
-  kern<<<static_cast<unsigned>(2 * pairs), Plan<EPI, F32>::kThreads, smem, st>>>(l.p);
-  return cudaGetLastError();
+  return launch_pdl(true, kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Plan<EPI, F32>::kThreads), smem, st, l.p);
 }
 
 template <bool F32, int NT, bool DUAL>
@@ -320,26 +335,33 @@ struct Ffn {
   }
   Mat weight(const void* p, long long rows, long long cols) const { return Mat{p, cols, rows, l.planes, cols, l.w_plane}; }
 
-  cudaError_t pack(const void* src, bf16* dst, long long B, long long rows, long long L, long long pitch,
-                   long long plane) const {
-    const long long blocks = cdiv(pitch / 8 * rows, 256);
-    k_ffn_pack<TT><<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, a.stream>>>(
-        static_cast<const TT*>(src), dst, rows, L, B * L, pitch, plane);
-    return cudaGetLastError();
-  }
-  cudaError_t pack_activation(const void* src, size_t at) const {
-    if (l.token) return F32 ? pack(src, wsb(at), 1, T, a.C, a.C, l.act_plane) : cudaSuccess;
-    return l.packed ? pack(src, wsb(at), a.B, a.C, a.L, l.pitch, l.act_plane) : cudaSuccess;
-  }
-  cudaError_t pack_weights() const {
-    if (!F32) return cudaSuccess;
-    const void* w[3] = {a.wg, a.wu, a.wd};
-    for (int i = 0; i < 3; ++i) {
-      const long long rows = i < 2 ? a.F : a.C, cols = i < 2 ? a.C : a.F;
-      const cudaError_t e = pack(w[i], wsb(l.w) + 3 * i * l.w_plane, 1, rows, cols, cols, l.w_plane);
-      if (e != cudaSuccess) return e;
+  // Everything of the call that is not read where it lies.
+  cudaError_t pack(bool backward) const {
+    Packs packs{};
+    int n = 0;
+    long long most = 0;
+    auto add = [&](const void* src, bf16* dst, long long B, long long rows, long long L, long long pitch, long long plane) {
+      packs.p[n++] = Pack{src, dst, rows, L, B * L, pitch, plane};
+      if (pitch / 8 * rows > most) most = pitch / 8 * rows;
+    };
+    const void* acts[2] = {a.x, a.dy};
+    const size_t to[2] = {l.x, l.dy};
+    for (int i = 0; i < (backward ? 2 : 1); ++i) {
+      if (l.packed)
+        add(acts[i], wsb(to[i]), a.B, a.C, a.L, l.pitch, l.act_plane);
+      else if (F32)
+        add(acts[i], wsb(to[i]), 1, T, a.C, a.C, l.act_plane);
     }
-    return cudaSuccess;
+    const void* w[3] = {a.wg, a.wu, a.wd};
+    for (int i = 0; F32 && i < 3; ++i) {
+      const long long rows = i < 2 ? a.F : a.C, cols = i < 2 ? a.C : a.F;
+      add(w[i], wsb(l.w) + 3 * i * l.w_plane, 1, rows, cols, cols, l.w_plane);
+    }
+    if (!n) return cudaSuccess;
+    const long long blocks = cdiv(most, 256);
+    k_ffn_pack<TT><<<dim3(static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8), static_cast<unsigned>(n)), 256, 0,
+                     a.stream>>>(packs);
+    return cudaGetLastError();
   }
 
   Launch start() const {
@@ -404,7 +426,7 @@ struct Ffn {
 
   cudaError_t forward() const {
     cudaError_t e;
-    if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_weights()) != cudaSuccess) return e;
+    if ((e = pack(false)) != cudaSuccess) return e;
     Launch h = start();
     h.p.seg[0] = gates_seg(h, hn, hn);
     hidden_out(h, 1);
@@ -420,9 +442,7 @@ struct Ffn {
 
   cudaError_t backward() const {
     cudaError_t e;
-    if ((e = pack_activation(a.x, l.x)) != cudaSuccess || (e = pack_activation(a.dy, l.dy)) != cudaSuccess ||
-        (e = pack_weights()) != cudaSuccess)
-      return e;
+    if ((e = pack(true)) != cudaSuccess) return e;
     // H, dG, dU
     Launch h = start();
         if (F32) {
@@ -486,12 +506,11 @@ struct Ffn {
       w.job(q);
     }
     if ((e = run<kEpiOut, F32>(w, a.stream)) != cudaSuccess) return e;
-    if (l.splits > 1)
-      for (int i = 0; i < 3; ++i) {
-        const long long blocks = cdiv(l.w_plane, 1024);
-        k_ffn_sum<TT><<<static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, a.stream>>>(
-            part + static_cast<size_t>(i) * l.splits * l.w_plane, static_cast<TT*>(out[i]), l.w_plane, l.splits);
-      }
+    if (l.splits > 1) {
+      const long long blocks = cdiv(l.w_plane, 1024);
+      k_ffn_sum<TT><<<dim3(static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8), 3), 256, 0, a.stream>>>(
+          part, Sums{{a.dwg, a.dwu, a.dwd}}, l.w_plane, l.splits);
+    }
     return cudaGetLastError();
   }
 };

@@ -30,7 +30,8 @@
 // ones first.  The tensor core truncates where it adds to an accumulator, a
 // loss that grows with the number of additions (measured: 1.0e-6 of the
 // result at depth 528, 1.4e-6 further on), so a loop is cut into pieces of
-// 128 whose sums the epilogue adds up in registers, to the nearest.
+// 256 whose sums the epilogue adds up to the nearest: in the other half of
+// tensor memory, or for the three hidden gradients in registers.
 #pragma once
 
 #include <cuda.h>
@@ -93,6 +94,7 @@ struct Params {
   int planes;                // 1, or 3 for fp32
   int a_plane, b_plane;      // third-coordinate distance of the planes
   int act;
+  int piece;                 // fp32: stages of each segment that the tensor core adds up
   // the hidden tensors [plane][batch][position][channel]
   __nv_bfloat16* hid[3];
   long long hid_plane, hid_rs;
@@ -217,6 +219,18 @@ __device__ __forceinline__ void tmem_load<16>(uint32_t (&r)[16], uint32_t addr) 
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, "
+      "%25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -436,9 +450,9 @@ struct Walk {
     hi = min(stages, lo + kper);
   }
 };
-template <int PIECE>
-__device__ __forceinline__ int pieces_of(int lo, int hi) {
-  return PIECE < 1 << 30 ? (hi - lo + PIECE - 1) / PIECE : 1;
+template <bool F32>
+__device__ __forceinline__ int pieces_of(const Params& p, int lo, int hi) {
+  return F32 ? (hi - lo + p.piece - 1) / p.piece : 1;
 }
 
 // Waits with the whole warp: all lanes go on or none.
@@ -456,11 +470,11 @@ template <int EPI, bool F32>
 struct Plan {
   static constexpr int kTurns = EPI == kEpiGrad && !F32 ? 2 : 1;    // of G and U in a tile
   static constexpr int kSegs = kTurns + 1;                          // segments of a job at most
-  static constexpr int kBufs = kTurns == 2 ? 1 : 2;                 // accumulators of 256 columns
-  static constexpr int kPiece = F32 ? 2 : 1 << 30;                  // stages added up in tensor memory
-  // columns of a tile: hidden channels, or columns of D.  fp32 has fewer: a
-  // thread holds its columns' sums in registers
-  static constexpr int kCols = F32 ? (EPI == kEpiOut ? 128 : 64) : EPI == kEpiHidden ? 128 : 256;
+  static constexpr bool kSums = F32 && EPI != kEpiGrad;             // pieces add up in the other accumulator
+  static constexpr int kBufs = kTurns == 2 || kSums ? 1 : 2;        // accumulators of 256 columns
+  // columns of a tile: hidden channels, or columns of D.  The fp32 gradients
+  // have fewer: a thread holds its columns' sums in registers
+  static constexpr int kCols = EPI == kEpiHidden ? 128 : F32 && EPI == kEpiGrad ? 64 : 256;
   static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;
   // Four warps of epilogue see all lanes; two such groups share the columns.
   static constexpr int kGroups = 2;
@@ -550,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
       const Tile ti = walk.tile(t);
       int lo, hi;
       walk.range(ti.split, lo, hi);
-      const int pieces = pieces_of<PL::kPiece>(lo, hi);
+      const int pieces = pieces_of<F32>(p, lo, hi);
       for (int pc = 0; ok && pc < pieces * combos; ++pc) {
         int plane = 0;
         if (F32) {
@@ -558,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
           planes_of(pc % combos, pa, pb);
           plane = is_b ? pb * p.b_plane : pa * p.a_plane;
         }
-        const int from = F32 ? lo + pc / combos * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
+        const int from = F32 ? lo + pc / combos * p.piece : lo, to = F32 ? min(hi, from + p.piece) : hi;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           if (i >= nseg || (i == 2 && ti.nt * 256 + 128 >= wide)) continue;      // no second turn behind the last channel
@@ -616,12 +630,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
         int lo, hi;
         walk.range(walk.split(t), lo, hi);
         // what is handed to the epilogue at a time: a piece of fp32's sums, or a turn of G and U
-        int pieces = pieces_of<PL::kPiece>(lo, hi);
+        int pieces = pieces_of<F32>(p, lo, hi);
         if (PL::kTurns == 2) pieces = walk.tile(t).nt * 256 + 128 < wide ? 2 : 1;
         for (int pc = 0; ok && pc < pieces; ++pc) {
           if (!(ok = warp_wait(acce + 8 * buf, bph ^ 1, p.status))) break;
           tmem_fence_after();
-          const int from = F32 ? lo + pc * PL::kPiece : lo, to = F32 ? min(hi, from + PL::kPiece) : hi;
+          const int from = F32 ? lo + pc * p.piece : lo, to = F32 ? min(hi, from + p.piece) : hi;
           for (int c = 0; ok && c < combos; ++c)
 #pragma unroll
             for (int i = 0; i < S; ++i) {
@@ -678,20 +692,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
       const int m0 = ti.mt * 256 + static_cast<int>(rank) * 128;
       const long long m = m0 + row;
       const bool live = m < j.M;
-      if constexpr (F32) {
-        // sum[q][i]: product q of the tile at this group's column i
-        constexpr int Q = EPI == kEpiOut ? 1 : EPI == kEpiHidden ? 2 : 3;
-        constexpr int W = PL::kCols / GR;
-        float sum[Q][W];
+      if constexpr (PL::kSums) {
         int lo, hi;
         walk.range(ti.split, lo, hi);
-        const int pieces = pieces_of<PL::kPiece>(lo, hi);
+        const int pieces = pieces_of<F32>(p, lo, hi);
+        const uint32_t acc = tmem + lanes;
+        // columns from c on, 32 of them: the last piece's on the sum of those before
+        auto gather = [&](uint32_t (&v)[32], int c, bool more) {
+          tmem_load(v, acc + c);
+          if (more) {
+            uint32_t before[32];
+            tmem_load(before, acc + 256 + c);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(before[i]));
+          } else {
+            tmem_wait_load();
+          }
+        };
+        // the columns of this group: of each product, kCols / 2
+        constexpr int Q = EPI == kEpiOut ? 1 : 2, PER = PL::kCols / GR;
+        bool yes = true;
+        for (int pc = 0; pc < pieces - 1 && (yes = arrived()); ++pc) {
+#pragma unroll 1
+          for (int c = 0; c < Q * PER; c += 32) {
+            const int col = c / PER * PL::kCols + group * PER + c % PER;
+            if (ti.nt * PL::kCols + group * PER + c % PER >= j.N) continue;      // no such columns
+            uint32_t v[32];
+            gather(v, col, pc > 0);
+            tmem_store(acc + 256 + col, v);
+          }
+          tmem_wait_store();
+          release();
+        }
+        if (!yes || !arrived()) break;
+        const bool more = pieces > 1;
+        if constexpr (EPI == kEpiOut) {
+          const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
+#pragma unroll 1
+          for (int c = 0; c < PER; c += 32) {
+            const int n0 = ti.nt * PL::kCols + group * PER + c;
+            uint32_t v[32];
+            if (n0 < j.N) gather(v, group * PER + c, more);
+            if (c + 32 == PER) release();
+            if (n0 >= j.N) continue;
+            if (j.kind == kOutF32) {
+              float* o = static_cast<float*>(j.ptr) + (j.splits > 1 ? ti.split * j.bs : 0) + at;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __uint_as_float(v[i]);
+            } else {
+              // token-major: a lane's columns are adjacent (N is a multiple of 8)
+              float* o = static_cast<float*>(j.ptr) + m * j.rs + n0;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                if (live && n0 + i < j.N)
+                  *HND_G(reinterpret_cast<uint4*>(o + i)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < PER; c += 32) {
+            const int n0 = ti.nt * PL::kCols + group * PER + c;
+            uint32_t g[32], u[32];
+            if (n0 < j.N) {
+              gather(g, group * PER + c, more);
+              gather(u, PL::kCols + group * PER + c, more);
+            }
+            if (c + 32 == PER) release();
+            if (n0 >= j.N) continue;
+            __nv_bfloat16* o = p.hid[0] + m * p.hid_rs + n0;
+            with_act(p.act, [&](auto kind) {
+              constexpr int ACT = decltype(kind)::value;
+#pragma unroll
+              for (int i0 = 0; i0 < 32; i0 += 8) {
+                uint32_t w[3][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int at = i0 + 2 * i;
+                  const float gv[2] = {__uint_as_float(g[at]), __uint_as_float(g[at + 1])};
+                  const float uv[2] = {__uint_as_float(u[at]), __uint_as_float(u[at + 1])};
+                  float h[2];
+                  hidden2<true, ACT>(gv, uv, h);
+                  split3x2(h[0], h[1], w[0][i], w[1][i], w[2][i]);
+                }
+                if (live && n0 + i0 < j.N)
+#pragma unroll
+                  for (int k = 0; k < 3; ++k)
+                    *HND_G(reinterpret_cast<uint4*>(o + k * p.hid_plane + i0)) =
+                        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+              }
+            });
+          }
+        }
+      } else if constexpr (F32) {
+        // sum[q][i]: product q of the tile at this group's column i
+        constexpr int W = PL::kCols / GR;
+        float sum[3][W];
+        int lo, hi;
+        walk.range(ti.split, lo, hi);
+        const int pieces = pieces_of<F32>(p, lo, hi);
         bool yes = true;
         for (int pc = 0; pc < pieces; ++pc) {
           if (!(yes = arrived())) break;
           const uint32_t acc = tmem + lanes + buf * 256 + group * W;
 #pragma unroll
-          for (int q = 0; q < Q; ++q)
+          for (int q = 0; q < 3; ++q)
 #pragma unroll
             for (int c0 = 0; c0 < W; c0 += 32) {
               uint32_t v[32];
@@ -705,56 +811,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
         }
         if (!yes) break;
         const int n0 = ti.nt * PL::kCols + group * W;
-        if constexpr (EPI == kEpiOut) {
-          if (j.kind == kOutF32) {
-            const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
-            float* o = static_cast<float*>(j.ptr) + (j.splits > 1 ? ti.split * j.bs : 0) + at;
+        __nv_bfloat16* o = p.hid[0] + m * p.hid_rs + n0;
+        const long long apart[3] = {0, p.hid[1] - p.hid[0], p.hid[2] - p.hid[0]};
+        with_act(p.act, [&](auto kind) {
+          constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-              if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = sum[0][i];
-          } else {
-            // token-major: a lane's columns are adjacent (N is a multiple of 8)
-            float* o = static_cast<float*>(j.ptr) + m * j.rs + n0;
+          for (int i = 0; i < W; i += 2) {      // the hidden values take the place of the sums
+            const float g[2] = {sum[0][i], sum[0][i + 1]}, u[2] = {sum[1][i], sum[1][i + 1]};
+            const float d[2] = {sum[2][i], sum[2][i + 1]};
+            float r[3][2];
+            hidden_grads2<true, ACT>(g, u, d, r[0], r[1], r[2]);
 #pragma unroll
-            for (int i = 0; i < W; i += 4)
-              if (live && n0 + i < j.N)
-                *HND_G(reinterpret_cast<float4*>(o + i)) =
-                    make_float4(sum[0][i], sum[0][i + 1], sum[0][i + 2], sum[0][i + 3]);
+            for (int q = 0; q < 3; ++q) sum[q][i] = r[q][0], sum[q][i + 1] = r[q][1];
           }
-        } else {
-          __nv_bfloat16* o = p.hid[0] + m * p.hid_rs + n0;
-          const long long apart[3] = {0, p.hid[1] - p.hid[0], p.hid[2] - p.hid[0]};
-          with_act(p.act, [&](auto kind) {
-            constexpr int ACT = decltype(kind)::value;
+        });
 #pragma unroll
-            for (int i = 0; i < W; i += 2) {      // the hidden values take the place of the sums
-              const float g[2] = {sum[0][i], sum[0][i + 1]}, u[2] = {sum[1][i], sum[1][i + 1]};
-              float r[3][2];
-              if constexpr (EPI == kEpiGrad) {
-                const float d[2] = {sum[2][i], sum[2][i + 1]};
-                hidden_grads2<true, ACT>(g, u, d, r[0], r[1], r[2]);
-              } else {
-                hidden2<true, ACT>(g, u, r[0]);
-              }
+        for (int q = 0; q < 3; ++q)
 #pragma unroll
-              for (int q = 0; q < PL::kOuts; ++q) sum[q][i] = r[q][0], sum[q][i + 1] = r[q][1];
-            }
-          });
+          for (int i0 = 0; i0 < W; i0 += 8) {
+            uint32_t w[3][4];
 #pragma unroll
-          for (int q = 0; q < PL::kOuts; ++q)
+            for (int i = 0; i < 4; ++i)
+              split3x2(sum[q][i0 + 2 * i], sum[q][i0 + 2 * i + 1], w[0][i], w[1][i], w[2][i]);
+            if (live && n0 + i0 < j.N)
 #pragma unroll
-            for (int i0 = 0; i0 < W; i0 += 8) {
-              uint32_t w[3][4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                split3x2(sum[q][i0 + 2 * i], sum[q][i0 + 2 * i + 1], w[0][i], w[1][i], w[2][i]);
-              if (live && n0 + i0 < j.N)
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                  *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
-                      make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-            }
-        }
+              for (int k = 0; k < 3; ++k)
+                *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
+                    make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+          }
       } else {
         if constexpr (EPI == kEpiOut) {
           if (!arrived()) break;
@@ -763,9 +847,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
           for (int c0 = 0; c0 < 128; c0 += 32) {
             const int n0 = ti.nt * 256 + group * 128 + c0;
             uint32_t v[32];
-            tmem_load(v, acc + c0);
-            tmem_wait_load();
+            if (n0 < j.N) {      // such columns exist
+              tmem_load(v, acc + c0);
+              tmem_wait_load();
+            }
             if (c0 == 96) release();
+            if (n0 >= j.N) continue;
             if (j.kind == kOutTma) {
               const uint32_t sb = stage + sbuf * PL::kStoreBytes;
               if (issuer) store_wait_read<1>();

@@ -115,8 +115,8 @@ struct Layout {
 // split, the partial sums go through memory once each way and one more
 // kernel runs.  C 256, F 1024, 32768 positions: 6 splits, 12 tiles otherwise
 // on 74 pairs; C 2048, F 5632: none (3 would add 67 us of partial sums).
-static int weight_splits(long long C, long long F, long long stages, int cols) {
-  const long long tiles = 2 * cdiv(C, 256) * cdiv(F, cols) + cdiv(F, 256) * cdiv(C, cols);
+static int weight_splits(long long C, long long F, long long stages) {
+  const long long tiles = 3 * cdiv(C, 256) * cdiv(F, 256);
   int best = 1;
   long long cost = 0;
   for (int s = 1; s <= 32 && (s == 1 || stages / s >= 4); ++s) {
@@ -167,7 +167,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   if (backward) {
     // every split gets a stage at least
     const long long stages = l.batches * cdiv(l.Lx, kBK);
-    const long long per = cdiv(stages, weight_splits(a.C, a.F, stages * (a.bf16 ? 1 : 6), a.bf16 ? 256 : 128));
+    const long long per = cdiv(stages, weight_splits(a.C, a.F, stages * (a.bf16 ? 1 : 6)));
     l.splits = static_cast<int>(cdiv(stages, per));
     if (l.splits > 1) l.part = take(3 * l.splits * l.w_plane, 4);
   }
@@ -368,6 +368,7 @@ struct Ffn {
     Launch n;
     n.p.planes = l.planes;
     n.p.act = a.act;
+    n.p.piece = 4;
     n.p.status = a.status;
     // plane distances in the third coordinate: a batched operand has its batches in between
     n.p.a_plane = n.p.b_plane = 1;
@@ -458,6 +459,7 @@ struct Ffn {
     if ((e = run<kEpiGrad, F32>(h, a.stream)) != cudaSuccess) return e;
     // dX
     Launch d = start();
+    d.p.piece = 2;      // of both its segments
     d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1);
     d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0);
     Job j = data_job(2, a.C, on, a.F);

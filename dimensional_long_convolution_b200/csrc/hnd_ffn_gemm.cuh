@@ -78,6 +78,7 @@ struct Job {
   // issuing warps took longer to find a short tile than its products do
   Div per, group8, mdiv;
   long long M, N;            // extents of D
+  int cols;                  // columns of a tile of kEpiOut: 256, 128 or 64
   int kind, map;             // how D leaves, and the map of kOutTma
   void* ptr;                 // D otherwise: element (m, n) of split s at
   long long bs, rs;          //   s bs + n rs + m, or with group > 0 at
@@ -710,14 +711,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
             tmem_wait_load();
           }
         };
-        // the columns of this group: of each product, kCols / 2
-        constexpr int Q = EPI == kEpiOut ? 1 : 2, PER = PL::kCols / GR;
+        // the columns of this group: of each product, half of a tile's
+        constexpr int Q = EPI == kEpiOut ? 1 : 2;
+        const int cols = EPI == kEpiOut ? pinned(j.cols) : PL::kCols, per = cols / GR;
         bool yes = true;
         for (int pc = 0; pc < pieces - 1 && (yes = arrived()); ++pc) {
 #pragma unroll 1
-          for (int c = 0; c < Q * PER; c += 32) {
-            const int col = c / PER * PL::kCols + group * PER + c % PER;
-            if (ti.nt * PL::kCols + group * PER + c % PER >= j.N) continue;      // no such columns
+          for (int c = 0; c < Q * per; c += 32) {
+            const int col = c / per * PL::kCols + group * per + c % per;
+            if (ti.nt * cols + group * per + c % per >= j.N) continue;      // no such columns
             uint32_t v[32];
             gather(v, col, pc > 0);
             tmem_store(acc + 256 + col, v);
@@ -730,11 +732,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
         if constexpr (EPI == kEpiOut) {
           const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
 #pragma unroll 1
-          for (int c = 0; c < PER; c += 32) {
-            const int n0 = ti.nt * PL::kCols + group * PER + c;
+          for (int c = 0; c < per; c += 32) {
+            const int n0 = ti.nt * cols + group * per + c;
             uint32_t v[32];
-            if (n0 < j.N) gather(v, group * PER + c, more);
-            if (c + 32 == PER) release();
+            if (n0 < j.N) gather(v, group * per + c, more);
+            if (c + 32 == per) release();
             if (n0 >= j.N) continue;
             if (j.kind == kOutF32) {
               float* o = static_cast<float*>(j.ptr) + (j.splits > 1 ? ti.split * j.bs : 0) + at;
@@ -752,14 +754,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < PER; c += 32) {
-            const int n0 = ti.nt * PL::kCols + group * PER + c;
+          for (int c = 0; c < per; c += 32) {
+            const int n0 = ti.nt * cols + group * per + c;
             uint32_t g[32], u[32];
             if (n0 < j.N) {
-              gather(g, group * PER + c, more);
-              gather(u, PL::kCols + group * PER + c, more);
+              gather(g, group * per + c, more);
+              gather(u, PL::kCols + group * per + c, more);
             }
-            if (c + 32 == PER) release();
+            if (c + 32 == per) release();
             if (n0 >= j.N) continue;
             __nv_bfloat16* o = p.hid[0] + m * p.hid_rs + n0;
             with_act(p.act, [&](auto kind) {
@@ -842,16 +844,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
       } else {
         if constexpr (EPI == kEpiOut) {
           if (!arrived()) break;
-          const uint32_t acc = tmem + lanes + buf * 256 + group * 128;
+          const int per = pinned(j.cols) / GR;
+          const uint32_t acc = tmem + lanes + buf * 256 + group * per;
           const long long at = j.group > 0 ? (m / j.group) * j.gs + m % j.group : m;
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            const int n0 = ti.nt * 256 + group * 128 + c0;
+          for (int c0 = 0; c0 < per; c0 += 32) {
+            const int n0 = ti.nt * per * GR + group * per + c0;
             uint32_t v[32];
             if (n0 < j.N) {      // such columns exist
               tmem_load(v, acc + c0);
               tmem_wait_load();
             }
-            if (c0 == 96) release();
+            if (c0 + 32 == per) release();
             if (n0 >= j.N) continue;
             if (j.kind == kOutTma) {
               const uint32_t sb = stage + sbuf * PL::kStoreBytes;

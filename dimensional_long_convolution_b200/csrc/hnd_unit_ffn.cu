@@ -110,13 +110,24 @@ struct Layout {
   int splits;
 };
 
+// Columns of the tiles of a product of `N` columns over `m_tiles` tiles of 256
+// rows: 256, unless there are fewer, or fewer tiles than half the pairs. An
+// MMA takes as long for 64 columns as for 256, so narrower tiles only pay
+// where pairs would be idle (3 x 777 positions, C 200, F 536: 10 tiles, the
+// second product 13 us with 256 columns, 10 with 64).
+static int tile_cols(long long N, long long m_tiles) {
+  int cols = 256;
+  while (cols > 64 && (N <= cols / 2 || m_tiles * cdiv(N, cols) < kPairs / 2)) cols /= 2;
+  return cols;
+}
+
 // Splits of the weight gradients' K loops.  In stages of a pair (0.27 us at
 // full rate): rounds of tiles, each with 8 stages' worth for a tile's ends;
 // split, the partial sums go through memory once each way and one more
 // kernel runs.  C 256, F 1024, 32768 positions: 6 splits, 12 tiles otherwise
 // on 74 pairs; C 2048, F 5632: none (3 would add 67 us of partial sums).
 static int weight_splits(long long C, long long F, long long stages) {
-  const long long tiles = 3 * cdiv(C, 256) * cdiv(F, 256);
+  const long long tiles = 2 * cdiv(C, 256) * cdiv(F, 256) + cdiv(F, 256) * cdiv(C, 256);
   int best = 1;
   long long cost = 0;
   for (int s = 1; s <= 32 && (s == 1 || stages / s >= 4); ++s) {
@@ -308,7 +319,7 @@ struct Ffn {
   using TT = typename std::conditional<F32, float, bf16>::type;
   // columns of a tile: hidden channels, and columns of the other products
   using PG = Plan<kEpiGrad, F32>;
-  static constexpr int hn = Plan<kEpiHidden, F32>::kCols, gn = PG::kCols, on = Plan<kEpiOut, F32>::kCols;
+  static constexpr int hn = Plan<kEpiHidden, F32>::kCols, gn = PG::kCols;
   const FfnArgs& a;
   const Layout l;
   const long long T;
@@ -394,6 +405,7 @@ struct Ffn {
     j.batches = static_cast<int>(l.batches);
     j.mt = static_cast<int>(cdiv(l.Lx, 256));
     j.nt = static_cast<int>(cdiv(N, per_tile));
+    j.cols = per_tile;
     j.splits = j.kbatches = 1;
     j.kblocks = j.kper = static_cast<int>(cdiv(depth, kBK));
     j.M = l.Lx;
@@ -434,6 +446,7 @@ struct Ffn {
     h.job(data_job(1, a.F, hn, a.C));
     if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
     Launch y = start();
+    const int on = tile_cols(a.C, l.batches * cdiv(l.Lx, 256));
     y.p.seg[0] = data_seg(y.km(hid[0]), y.km(wd, on / 2), false, false, on, 0, 1);
     Job j = data_job(1, a.C, on, a.F);
     activation_out(y, j, a.y);
@@ -460,6 +473,7 @@ struct Ffn {
     // dX
     Launch d = start();
     d.p.piece = 2;      // of both its segments
+    const int on = tile_cols(a.C, l.batches * cdiv(l.Lx, 256));
     d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1);
     d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0);
     Job j = data_job(2, a.C, on, a.F);
@@ -470,14 +484,15 @@ struct Ffn {
     Launch w = start();
     const bool batched = l.batches > 1;
     const int stages = static_cast<int>(cdiv(l.Lx, kBK));
-    const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, on / 2);
+    const int cg = tile_cols(a.F, kPairs), cd = tile_cols(a.C, kPairs);
+    const int mx = l.token ? w.mn(x) : w.km(x), mdy = l.token ? w.mn(dy) : w.km(dy, cd / 2);
     const int mh = w.mn(hid[0]), mdg = w.mn(hid[1]), mdu = w.mn(hid[2]);
-    auto seg = [&](int ma, int mb, int a_mn, int b_mn) {
-      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, on, on, on / 2, 0, 0, 1};
+    auto seg = [&](int ma, int mb, int a_mn, int b_mn, int cols) {
+      return Seg{ma, mb, mb, a_mn, b_mn, batched, batched, cols, cols, cols / 2, 0, 0, 1};
     };
-    w.p.seg[0] = seg(mx, mdg, l.token, 1);
-    w.p.seg[1] = seg(mx, mdu, l.token, 1);
-    w.p.seg[2] = seg(mh, mdy, 1, l.token);
+    w.p.seg[0] = seg(mx, mdg, l.token, 1, cg);
+    w.p.seg[1] = seg(mx, mdu, l.token, 1, cg);
+    w.p.seg[2] = seg(mh, mdy, 1, l.token, cd);
     void* out[3] = {a.dwg, a.dwu, a.dwd};
     float* part = reinterpret_cast<float*>(ws(l.part));
     for (int i = 0; i < 3; ++i) {
@@ -487,7 +502,8 @@ struct Ffn {
       q.M = i < 2 ? a.C : a.F;
       q.N = i < 2 ? a.F : a.C;
       q.mt = static_cast<int>(cdiv(q.M, 256));
-      q.nt = static_cast<int>(cdiv(q.N, on));
+      q.cols = i < 2 ? cg : cd;
+      q.nt = static_cast<int>(cdiv(q.N, q.cols));
       q.batches = 1;
       q.kbatches = static_cast<int>(l.batches);
       q.kblocks = stages;

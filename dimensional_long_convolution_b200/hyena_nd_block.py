@@ -16,7 +16,6 @@ torch operation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -119,34 +118,46 @@ class _GridOp:
         self.shape = torch.Size((self.B, self.C) + self.dims)
         self.s = Shape(self.B, self.C, math.prod(self.dims), H.BF16 if io_dtype == "bf16" else H.F32)
         self.lib = load()
-
-    def _here(self):
-        """The object's device as the current one (launches go to the current device)."""
-        if self.device.type != "cuda" or self.torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return self.torch.cuda.device(self.device)
+        self.ref = ctypes.byref(self.s)
+        # the current stream's handle without a Stream object around it (4 us a call less), where torch has that
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def _stream(self) -> int:
+        if self.device.type != "cuda":
+            raise ValueError("the operators run on CUDA devices, not on %s" % self.device)
+        if self.raw_stream is not None:
+            return self.raw_stream(self.device.index)
         return self.torch.cuda.current_stream(self.device).cuda_stream
 
-    def _check(self, **tensors) -> None:
-        """Activations: contiguous, of the problem's shape, dtype and device."""
-        for name, t in tensors.items():
-            if t.shape != self.shape or t.dtype != self.tdtype or t.device != self.device or not t.is_contiguous():
-                raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                                 % (name, self.tdtype, tuple(self.shape), self.device))
+    def _run(self, call, what: str, *args) -> None:
+        """A library call on the current stream of the object's device, which
+        launches need as the current one."""
+        cuda, stream = self.torch.cuda, self._stream()
+        if cuda.current_device() == self.device.index:
+            code = call(*args, stream)
+        else:
+            with cuda.device(self.device):
+                code = call(*args, stream)
+        if code != H.OK:
+            raise H.HyenaNDError(code, what)
 
-    def _check_param(self, name: str, t, shape, dtype=None) -> None:
-        dtype = self.torch.float32 if dtype is None else dtype
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+    def _check(self, name: str, t) -> int:
+        """An activation (contiguous, of the problem's shape, dtype and device); its address."""
+        if t.shape != self.shape or t.dtype != self.tdtype or t.device != self.device or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                             % (name, self.tdtype, tuple(self.shape), self.device))
+        return t.data_ptr()
+
+    def _check_param(self, name: str, t, shape, dtype) -> int:
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
             raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                              % (name, dtype, tuple(shape), self.device))
+        return t.data_ptr()
 
     def _check_rng(self, rng) -> int:
         if rng is None:
             raise ValueError("dropout needs rng, an int64 tensor (seed, offset)")
-        self._check_param("rng", rng, (2,), self.torch.int64)
-        return rng.data_ptr()
+        return self._check_param("rng", rng, (2,), self.torch.int64)
 
     def _scratch(self, nbytes: int):
         return self.torch.empty(max(nbytes, 16), dtype=self.torch.uint8, device=self.device)
@@ -181,6 +192,7 @@ class BlockJoin(_GridOp):
         self.j.post.kind, self.j.pre.kind = NORM_KINDS[post], NORM_KINDS[pre]
         self.j.post.eps = self.j.pre.eps = float(eps)
         self.j.p = self.p
+        self.jref = ctypes.byref(self.j)
         self.ws_bytes = int(self.lib.hyena_nd_join_workspace_bytes(ctypes.byref(self.s)))
         if self.ws_bytes == 0:
             raise H.HyenaNDError(H.ERR_UNSUPPORTED, "join_workspace_bytes")
@@ -192,93 +204,78 @@ class BlockJoin(_GridOp):
                 continue
             if getattr(self, name.split("_")[0], "") == "none":
                 raise ValueError("%s given, but there is no such norm" % name)
-            self._check_param(name, t, (self.B, self.C) if name == "gate" else (self.C,))
+            self._check_param(name, t, (self.B, self.C) if name == "gate" else (self.C,), self.torch.float32)
         self.params = given
         ptr = {k: None if t is None else t.data_ptr() for k, t in given.items()}
         self.j.post.w, self.j.post.b = ptr["post_w"], ptr["post_b"]
         self.j.pre.w, self.j.pre.b = ptr["pre_w"], ptr["pre_b"]
         self.j.gate, self.j.scale = ptr["gate"], ptr["scale"]
 
-    def _with_rng(self, rng) -> Join:
+    def _with_rng(self, rng):
         if not self.drops:
-            return self.j
+            return self.jref
         j = Join.from_buffer_copy(self.j)       # one object may be called from several threads
         j.rng = self._check_rng(rng)
-        return j
+        return ctypes.byref(j)
 
     def __call__(self, x, y, rng=None, h=None, n=None):
         """(h, n); n is None without a pre norm."""
-        self._check(x=x, y=y)
-        h = self.torch.empty_like(x) if h is None else h
-        self._check(h=h)
-        if self.pre == "none":
-            if n is not None:
-                raise ValueError("n given, but there is no pre norm")
-        else:
-            n = self.torch.empty_like(x) if n is None else n
-            self._check(n=n)
+        xp, yp = self._check("x", x), self._check("y", y)
         j = self._with_rng(rng)
-        with self._here():
-            H.check(self.lib.hyena_nd_join_forward(ctypes.byref(self.s), ctypes.byref(j), x.data_ptr(), y.data_ptr(),
-                                                   h.data_ptr(), None if n is None else n.data_ptr(),
-                                                   self._stream()), "join_forward")
+        if n is not None and self.pre == "none":
+            raise ValueError("n given, but there is no pre norm")
+        h = self.torch.empty_like(x) if h is None else h
+        if n is None and self.pre != "none":
+            n = self.torch.empty_like(x)
+        self._run(self.lib.hyena_nd_join_forward, "join_forward", self.ref, j, xp, yp, self._check("h", h),
+                  None if n is None else self._check("n", n))
         return h, n
 
     def backward(self, x, y, dh, dn=None, rng=None) -> dict:
         """Gradients "dx", "dy" and "d" + name for each parameter that is set.
         dh: gradient that reaches h past the pre norm (None: zero); dn: that
         of n (exactly where there is a pre norm)."""
-        self._check(x=x, y=y)
+        xp, yp = self._check("x", x), self._check("y", y)
         if (dn is None) != (self.pre == "none"):
             raise ValueError("dn goes with the pre norm")
-        if dh is not None:
-            self._check(dh=dh)
-        if dn is not None:
-            self._check(dn=dn)
+        dhp = None if dh is None else self._check("dh", dh)
+        dnp = None if dn is None else self._check("dn", dn)
+        j = self._with_rng(rng)
         torch = self.torch
         out = {"dx": torch.empty_like(x), "dy": torch.empty_like(x)}
         grads = JoinGrads()
         for name, t in self.params.items():
             if t is not None:
-                out["d" + name] = torch.empty_like(t)
-                setattr(grads, name, out["d" + name].data_ptr())
+                out["d" + name] = g = torch.empty_like(t)
+                setattr(grads, name, g.data_ptr())
         ws = self._scratch(self.ws_bytes)
-        j = self._with_rng(rng)
-        with self._here():
-            H.check(self.lib.hyena_nd_join_backward(ctypes.byref(self.s), ctypes.byref(j), x.data_ptr(), y.data_ptr(),
-                                                    None if dh is None else dh.data_ptr(),
-                                                    None if dn is None else dn.data_ptr(), out["dx"].data_ptr(),
-                                                    out["dy"].data_ptr(), ctypes.byref(grads), ws.data_ptr(),
-                                                    ws.numel(), self._stream()), "join_backward")
+        self._run(self.lib.hyena_nd_join_backward, "join_backward", self.ref, j, xp, yp, dhp, dnp,
+                  out["dx"].data_ptr(), out["dy"].data_ptr(), ctypes.byref(grads), ws.data_ptr(), self.ws_bytes)
         return out
 
     def norm(self, x, n=None):
         """norm_pre(x) alone: the head of a stack."""
         if self.pre == "none":
             raise ValueError("there is no pre norm")
-        self._check(x=x)
+        xp = self._check("x", x)
         n = self.torch.empty_like(x) if n is None else n
-        self._check(n=n)
-        with self._here():
-            H.check(self.lib.hyena_nd_norm_forward(ctypes.byref(self.s), ctypes.byref(self.j.pre), x.data_ptr(),
-                                                   n.data_ptr(), self._stream()), "norm_forward")
+        self._run(self.lib.hyena_nd_norm_forward, "norm_forward", self.ref, ctypes.byref(self.j.pre), xp,
+                  self._check("n", n))
         return n
 
     def norm_backward(self, x, dn) -> dict:
         """Gradients "dx" and "dpre_w", "dpre_b" where set, of norm(x) for dn."""
         if self.pre == "none":
             raise ValueError("there is no pre norm")
-        self._check(x=x, dn=dn)
+        xp, dnp = self._check("x", x), self._check("dn", dn)
         out = {"dx": self.torch.empty_like(x)}
         for name in ("pre_w", "pre_b"):
             if self.params[name] is not None:
                 out["d" + name] = self.torch.empty_like(self.params[name])
         dw, db = (out[k].data_ptr() if k in out else None for k in ("dpre_w", "dpre_b"))
         ws = self._scratch(self.ws_bytes)
-        with self._here():
-            H.check(self.lib.hyena_nd_norm_backward(ctypes.byref(self.s), ctypes.byref(self.j.pre), x.data_ptr(),
-                                                    dn.data_ptr(), out["dx"].data_ptr(), dw, db, ws.data_ptr(),
-                                                    ws.numel(), self._stream()), "norm_backward")
+        self._run(self.lib.hyena_nd_norm_backward, "norm_backward", self.ref, ctypes.byref(self.j.pre), xp, dnp,
+                  out["dx"].data_ptr(), dw, db, ws.data_ptr(), self.ws_bytes)
         return out
 
 
@@ -297,13 +294,10 @@ class GridDropout(_GridOp):
         self.drops = math.floor(self.p * 65536 + 0.5) > 0
 
     def __call__(self, x, rng=None, y=None):
-        self._check(x=x)
-        y = self.torch.empty_like(x) if y is None else y
-        self._check(y=y)
+        xp = self._check("x", x)
         ptr = self._check_rng(rng) if self.drops else None
-        with self._here():
-            H.check(self.lib.hyena_nd_dropout(ctypes.byref(self.s), self.p, ptr, x.data_ptr(), y.data_ptr(),
-                                              self._stream()), "dropout")
+        y = self.torch.empty_like(x) if y is None else y
+        self._run(self.lib.hyena_nd_dropout, "dropout", self.ref, self.p, ptr, xp, self._check("y", y))
         return y
 
     def backward(self, dy, rng=None, dx=None):
@@ -327,38 +321,32 @@ class GatedFFN(_GridOp):
         if 0 in self.ws_bytes:
             raise H.HyenaNDError(H.ERR_UNSUPPORTED, "ffn_workspace_bytes")
         self.control = self.torch.zeros(256, dtype=self.torch.uint8, device=self.device)
+        self.fref = ctypes.byref(self.f)
+        self.up, self.down = self.torch.Size((self.F, self.C)), self.torch.Size((self.C, self.F))
 
-    def _check_weights(self, wg, wu, wd) -> None:
-        self._check_param("wg", wg, (self.F, self.C), self.tdtype)
-        self._check_param("wu", wu, (self.F, self.C), self.tdtype)
-        self._check_param("wd", wd, (self.C, self.F), self.tdtype)
+    def _check_weights(self, wg, wu, wd):
+        return (self._check_param("wg", wg, self.up, self.tdtype), self._check_param("wu", wu, self.up, self.tdtype),
+                self._check_param("wd", wd, self.down, self.tdtype))
 
     def __call__(self, x, wg, wu, wd, y=None):
-        self._check(x=x)
-        self._check_weights(wg, wu, wd)
+        xp, w = self._check("x", x), self._check_weights(wg, wu, wd)
         y = self.torch.empty_like(x) if y is None else y
-        self._check(y=y)
         ws = self._scratch(self.ws_bytes[0])
-        with self._here():
-            H.check(self.lib.hyena_nd_ffn_forward(ctypes.byref(self.f), x.data_ptr(), wg.data_ptr(), wu.data_ptr(),
-                                                  wd.data_ptr(), y.data_ptr(), self.control.data_ptr(),
-                                                  ws.data_ptr(), ws.numel(), self._stream()), "ffn_forward")
+        self._run(self.lib.hyena_nd_ffn_forward, "ffn_forward", self.fref, xp, *w, self._check("y", y),
+                  self.control.data_ptr(), ws.data_ptr(), self.ws_bytes[0])
         return y
 
     def backward(self, x, wg, wu, wd, dy):
         """(dx, dwg, dwu, dwd) for dy; the hidden activations are recomputed."""
-        self._check(x=x, dy=dy)
-        self._check_weights(wg, wu, wd)
-        out = [self.torch.empty_like(t) for t in (x, wg, wu, wd)]
+        xp, dyp, w = self._check("x", x), self._check("dy", dy), self._check_weights(wg, wu, wd)
+        out = tuple(self.torch.empty_like(t) for t in (x, wg, wu, wd))
         ws = self._scratch(self.ws_bytes[1])
-        with self._here():
-            H.check(self.lib.hyena_nd_ffn_backward(ctypes.byref(self.f), x.data_ptr(), wg.data_ptr(), wu.data_ptr(),
-                                                   wd.data_ptr(), dy.data_ptr(), *(t.data_ptr() for t in out),
-                                                   self.control.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                   self._stream()), "ffn_backward")
-        return tuple(out)
+        self._run(self.lib.hyena_nd_ffn_backward, "ffn_backward", self.fref, xp, *w, dyp,
+                  *(t.data_ptr() for t in out), self.control.data_ptr(), ws.data_ptr(), self.ws_bytes[1])
+        return out
 
     def status(self) -> int:
         """Waits for the current stream, then reads and clears the device-side status."""
-        with self._here():
-            return H.device_status(self.control.data_ptr(), self._stream())
+        stream = self._stream()
+        with self.torch.cuda.device(self.device):
+            return H.device_status(self.control.data_ptr(), stream)

@@ -289,6 +289,8 @@ def test_wrapper_refusals():
         op.set_params(gate=torch.ones(3))
     with pytest.raises(ValueError):
         op.set_params(scale=torch.ones(3, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        op(x, x.clone(), rng)                               # host tensors: nothing is launched
     ffn = K.GatedFFN((4,), 2, 8, 16, io_dtype="f32", device=cpu)
     with pytest.raises(ValueError):
         ffn(torch.zeros(2, 8, 4), torch.zeros(16, 8), torch.zeros(8, 16), torch.zeros(8, 16))

@@ -85,10 +85,17 @@ def measured_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# the operators around the convolution: no part of a step here
+BLOCK_SOURCES = ("hnd_block", "hnd_div", "hnd_ffn", "hnd_io", "hnd_join", "hnd_philox", "hnd_unit_dropout",
+                 "hnd_unit_ffn", "hnd_unit_join")
+
+
 def kernel_source_sha() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "dimensional_long_convolution_b200", "csrc")
     for name in sorted(os.listdir(csrc)):
+        if name.startswith(BLOCK_SOURCES):
+            continue
         if name.endswith((".cu", ".cuh", ".h", ".inc")) and name != "hnd_twiddles.inc":
             with open(os.path.join(csrc, name), "rb") as fh:
                 h.update(name.encode() + fh.read())

@@ -131,8 +131,7 @@ hyena_nd_status join_backward(const hyena_nd_block_shape* s, hnd::JoinArgs& a, v
   a.ws = ws;
   return bounds({{a.x, act}, {a.y, act}, {a.dh, act}, {a.dn, act}, {a.post.w, C4}, {a.post.b, C4}, {a.gate, BC4},
                  {a.scale, C4}, {a.pre.w, C4}, {a.pre.b, C4}, {a.drop.rng, 16}, {a.dx, act}, {a.dy, act},
-                 {a.dpost_w, C4}, {a.dpost_b, C4}, {a.dgate, BC4}, {a.dscale, C4}, {a.dpre_w, C4}, {a.dpre_b, C4},
-                 {ws, need}},
+                 {a.dgate, BC4}, {ws, need}},
                 nullptr, a.stream);
 }
 

@@ -21,7 +21,7 @@
 
 namespace hnd {
 
-constexpr int kBoundsMax = 24;
+constexpr int kBoundsMax = 16;
 
 struct BoundsTable {
   unsigned long long base[kBoundsMax];

@@ -12,7 +12,9 @@
 // run of the block.
 //
 // W neighbouring lanes hold 16 bytes of positions each, the rest of the 256
-// threads the channels, K apiece.
+// threads the channels, K apiece.  The loops over a thread's channels have no
+// branches, so that the K of them overlap: a channel that does not exist has
+// zeros in its slots and factors, and counts for nothing in a variance.
 //
 // Rows that do not start on 16 bytes (RAG) come as the aligned vectors that
 // cover them, one more than the lanes, and every thread shifts its positions
@@ -140,9 +142,9 @@ __device__ __forceinline__ void put_some(TT* p, const uint4& a, unsigned bits) {
 }
 
 // Shared memory: slots [tensor][K][rows][w, and one more if ragged] of 16
-// bytes, factors [C], sums.
-inline size_t smem_bytes(int tensors, int K, long long C, int w, int V, bool ragged) {
-  return static_cast<size_t>(tensors) * K * (kT + (ragged ? kT / w : 0)) * 16 + static_cast<size_t>(C) * 16 +
+// bytes, factors [K][rows], sums.
+inline size_t smem_bytes(int tensors, int K, int w, int V, bool ragged) {
+  return static_cast<size_t>(tensors) * K * (kT + (ragged ? kT / w : 0)) * 16 + static_cast<size_t>(K) * (kT / w) * 16 +
          sizeof(float) * (kWarps + 1) * 2 * w * V;
 }
 
@@ -157,7 +159,8 @@ struct Spot {
   bool next;
 };
 
-template <class TT, int K, bool RAG>
+// FIX: the block keeps to one sample, whose gate goes into the factors.
+template <class TT, int K, bool RAG, bool FIX>
 struct Grid {
   static constexpr int Q = Vec<TT>::Q, V = 2 * Q;
   const JoinDev& j;
@@ -166,11 +169,12 @@ struct Grid {
   long long own, step;              // of its first channel in a sample, and from one of its channels to the next
   uint4* slots;                     // its own
   int pitch;                        // slots from one k to the next
-  float4* coef;                     // of a channel: scale w1, scale b1, w2, b2
+  float4* coef;                     // of a channel: scale w1, scale b1 (times the gate, FIX), w2, b2
+  DropState ds{};
   float* part;                      // [kWarps][2 V w]
   float* total;                     // [2 V w]
 
-  __device__ Grid(const JoinDev& jj, int lanes, int tensors, unsigned char* smem)
+  __device__ Grid(const JoinDev& jj, int lanes, int tensors, unsigned char* smem, long long sample)
       : j(jj), w(lanes), lane(threadIdx.x % lanes), cg(threadIdx.x / lanes), rows(kT / lanes), C(static_cast<int>(jj.C)) {
 #pragma unroll
     for (int k = 0; k < K; ++k) chans |= static_cast<unsigned>(chan(k) < C) << k;
@@ -179,19 +183,34 @@ struct Grid {
     pitch = kT + (RAG ? rows : 0);
     slots = reinterpret_cast<uint4*>(smem) + cg * (w + RAG) + lane;
     coef = reinterpret_cast<float4*>(reinterpret_cast<uint4*>(smem) + tensors * K * pitch);
-    part = reinterpret_cast<float*>(coef + C);
+    part = reinterpret_cast<float*>(coef + K * rows);
     total = part + kWarps * 2 * V * w;
-    for (int c = threadIdx.x; c < C; c += kT) {
-      const float sc = j.scale ? __ldg(HND_G(j.scale + c)) : 1.f;
-      *HND_S(coef + c) = make_float4(sc * (j.w1 ? __ldg(HND_G(j.w1 + c)) : 1.f), sc * (j.b1 ? __ldg(HND_G(j.b1 + c)) : 0.f),
-                                     j.w2 ? __ldg(HND_G(j.w2 + c)) : 1.f, j.b2 ? __ldg(HND_G(j.b2 + c)) : 0.f);
+    for (int c = threadIdx.x; c < K * rows; c += kT) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < C) {
+        float sc = j.scale ? __ldg(HND_G(j.scale + c)) : 1.f;
+        if (FIX && j.gate) sc *= __ldg(HND_G(j.gate + sample * C + c));
+        f.x = sc * (j.w1 ? __ldg(HND_G(j.w1 + c)) : 1.f);
+        f.y = sc * (j.b1 ? __ldg(HND_G(j.b1 + c)) : 0.f);
+        f.z = j.w2 ? __ldg(HND_G(j.w2 + c)) : 1.f;
+        f.w = j.b2 ? __ldg(HND_G(j.b2 + c)) : 0.f;
+      }
+      *HND_S(coef + c) = f;
     }
+    if (j.border) ds = drop_state(j.rng);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (!there(k))
+        for (int i = 0; i < tensors; ++i)
+          for (int e = 0; e < (RAG && lane == w - 1 ? 2 : 1); ++e)      // the row's extra slot too
+            *HND_S(slots + (i * K + k) * pitch + e) = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
   __device__ int chan(int k) const { return cg + k * rows; }
+  __device__ bool there(int k) const { return chans >> k & 1u; }
   __device__ uint4 raw(int tensor, int k) const { return *HND_S(slots + (tensor * K + k) * pitch); }
   __device__ float gate(const Spot& s, int k) const {
-    return j.gate ? __ldg(HND_G(j.gate + static_cast<long long>(s.b) * C + chan(k))) : 1.f;
+    return !FIX && j.gate && there(k) ? __ldg(HND_G(j.gate + static_cast<long long>(s.b) * C + chan(k))) : 1.f;
   }
   // Ragged: how far into its aligned vector the lane's first position lies.
   __device__ int shift(const Spot& s, int k) const {
@@ -274,7 +293,7 @@ struct Grid {
   }
 
   // The eight mask bits of a group.
-  __device__ unsigned group_bits(const DropState& ds, long long group) const {
+  __device__ unsigned group_bits(long long group) const {
     const uint4 v = drop_lots(ds, static_cast<uint64_t>(group));
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     unsigned bits = 0;
@@ -286,21 +305,20 @@ struct Grid {
   }
   // keep[k]: a bit for each of the lane's positions.  All lanes take part.
   __device__ void mask(const Spot& s, unsigned (&keep)[K]) const {
-    const DropState ds = drop_state(j.rng);
     if constexpr (V == 8 && !RAG) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) keep[k] = group_bits(ds, (s.at + k * step) >> 3);
+      for (int k = 0; k < K; ++k) keep[k] = group_bits((s.at + k * step) >> 3);
     } else if constexpr (V == 8) {
       // lane i has group i of the row's tile; of the group behind the last lane's, lane q takes channel q / rows of a
       // warp in row q % rows
       const int rw = 32 / w, q = threadIdx.x & 31, row = q / w;
 #pragma unroll
-      for (int k = 0; k < K; ++k) keep[k] = group_bits(ds, (s.at + k * step) >> 3);
+      for (int k = 0; k < K; ++k) keep[k] = group_bits((s.at + k * step) >> 3);
       unsigned behind[K];
       for (int done = 0; done < K * rw; done += 32) {
         const int k = (done + q) / rw, r = (done + q) % rw;
         const long long at0 = __shfl_sync(0xFFFFFFFFu, s.at, r * w + w - 1);      // of that row's last lane
-        const unsigned got = k < K ? group_bits(ds, ((at0 + k * step) >> 3) + 1) : 0u;
+        const unsigned got = k < K ? group_bits(((at0 + k * step) >> 3) + 1) : 0u;
 #pragma unroll
         for (int i = 0; i < K; ++i) {
           const int from = i * rw + row - done;
@@ -319,7 +337,7 @@ struct Grid {
       const int odd = lane & 1;
 #pragma unroll
       for (int k = 0; k + 1 < K; k += 2) {
-        const unsigned mine = group_bits(ds, (s.at + (k + odd) * step) >> 3);
+        const unsigned mine = group_bits((s.at + (k + odd) * step) >> 3);
         const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
         keep[k] = (odd ? other : mine) >> (4 * odd);
         keep[k + 1] = (odd ? mine : other) >> (4 * odd);
@@ -328,8 +346,8 @@ struct Grid {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const long long e = s.at + k * step;
-        unsigned bits = group_bits(ds, e >> 3);
-        if (RAG && (e & 7) > 4) bits |= group_bits(ds, (e >> 3) + 1) << 8;
+        unsigned bits = group_bits(e >> 3);
+        if (RAG && (e & 7) > 4) bits |= group_bits((e >> 3) + 1) << 8;
         keep[k] = bits >> (e & 7);
       }
     }
@@ -373,7 +391,7 @@ struct Grid {
   }
   // Mean (negative) and reciprocal deviation of f(k, q) at each position.
   template <class Fn>
-  __device__ void stats(const Spot& at, int kind, float eps, float2 (&neg)[Q], float2 (&rho)[Q], Fn f) const {
+  __device__ void stats(int kind, float eps, float2 (&neg)[Q], float2 (&rho)[Q], Fn f) const {
 #pragma unroll
     for (int q = 0; q < Q; ++q) neg[q] = both(0.f), rho[q] = both(1.f);
     if (!kind) return;
@@ -384,7 +402,7 @@ struct Grid {
       for (int q = 0; q < Q; ++q) s[0][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (at.on >> k & 1u) f(k, [&](int q, float2 v) { s[0][q] = add(s[0][q], v); });
+        f(k, [&](int q, float2 v) { s[0][q] = add(s[0][q], v); });
       sum(s);
 #pragma unroll
       for (int q = 0; q < Q; ++q) neg[q] = mul(s[0][q], both(-inv));
@@ -392,12 +410,14 @@ struct Grid {
 #pragma unroll
     for (int q = 0; q < Q; ++q) s[0][q] = both(0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (at.on >> k & 1u)
-        f(k, [&](int q, float2 v) {
-          const float2 d = add(v, neg[q]);
-          s[0][q] = fma(d, d, s[0][q]);
-        });
+    for (int k = 0; k < K; ++k) {
+      const float2 counts = both(there(k) ? 1.f : 0.f);
+      f(k, [&](int q, float2 v) {
+        float2 d = v;
+        if (kind == 2) d = mul(add(v, neg[q]), counts);
+        s[0][q] = fma(d, d, s[0][q]);
+      });
+    }
     sum(s);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
@@ -405,41 +425,48 @@ struct Grid {
   }
 
   // y's statistics, the dropout bits and h.  Slots: 0 x, 1 y.
-  __device__ void head(const Spot& at, bool has_y, unsigned (&keep)[K], float2 (&hv)[K][Q], float2 (&neg)[Q], float2 (&rho)[Q]) const {
+  __device__ void head(const Spot& at, bool has_y, unsigned (&keep)[K], float2 (&hv)[K][Q], float2 (&neg)[Q],
+                       float2 (&rho)[Q]) const {
     if (!has_y) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (at.on >> k & 1u) {
-          const uint4 x = raw(0, k);
+      for (int k = 0; k < K; ++k) {
+        const uint4 x = raw(0, k);
 #pragma unroll
-          for (int q = 0; q < Q; ++q) hv[k][q] = Vec<TT>::get(x, q);
-        }
+        for (int q = 0; q < Q; ++q) hv[k][q] = Vec<TT>::get(x, q);
+      }
       return;
     }
-    stats(at, j.post, j.eps1, neg, rho, [&](int k, auto use) {
+    stats(j.post, j.eps1, neg, rho, [&](int k, auto use) {
       const uint4 y = raw(1, k);
 #pragma unroll
       for (int q = 0; q < Q; ++q) use(q, Vec<TT>::get(y, q));
     });
-    if (j.border) mask(at, keep);
+    if (j.border) {
+      mask(at, keep);
+      joined<true>(at, keep, hv, neg, rho);
+    } else {
+      joined<false>(at, keep, hv, neg, rho);
+    }
+  }
+  template <bool DROP>
+  __device__ void joined(const Spot& at, const unsigned (&keep)[K], float2 (&hv)[K][Q], const float2 (&neg)[Q],
+                         const float2 (&rho)[Q]) const {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!(at.on >> k & 1u)) continue;
       const uint4 x = raw(0, k), y = raw(1, k);
       const float4 cf = *HND_S(coef + chan(k));
       const float g = gate(at, k) * j.factor;
       const float2 al = both(cf.x * g), be = both(cf.y * g);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const float2 xv = Vec<TT>::get(x, q);
         float2 v = fma(mul(add(Vec<TT>::get(y, q), neg[q]), rho[q]), al, be);
-        if (j.border) {
-          v.x = (keep[k] >> (2 * q) & 1u) ? v.x : 0.f;
-          v.y = (keep[k] >> (2 * q + 1) & 1u) ? v.y : 0.f;
-        }
-        hv[k][q] = add(xv, v);
+        if (DROP) v = kept(keep[k], q, v);
+        hv[k][q] = add(Vec<TT>::get(x, q), v);
       }
     }
+  }
+  static __device__ float2 kept(unsigned bits, int q, float2 v) {
+    return make_float2((bits >> (2 * q) & 1u) ? v.x : 0.f, (bits >> (2 * q + 1) & 1u) ? v.y : 0.f);
   }
 };
 
@@ -448,9 +475,9 @@ __global__ void __launch_bounds__(kT, RAG ? 2 : 3) k_join_grid_fwd(const JoinDev
                                                          const TT* __restrict__ x, const TT* __restrict__ y,
                                                          TT* __restrict__ h, TT* __restrict__ n) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
-  using G = Grid<TT, K, RAG>;
+  using G = Grid<TT, K, RAG, false>;
   constexpr int Q = G::Q;
-  const G t(j, w, 2, hnd_dyn_smem);
+  const G t(j, w, 2, hnd_dyn_smem, 0);
   // Vectors of positions are counted through the samples, `per` to each, and a
   // tile takes w of them; ragged, a tile keeps to one sample and `per` counts
   // its tiles.
@@ -479,17 +506,15 @@ __global__ void __launch_bounds__(kT, RAG ? 2 : 3) k_join_grid_fwd(const JoinDev
       for (int k = 0; k < K; ++k)
         t.store(at, h, k, hv[k]);
     if (n) {
-      t.stats(at, j.pre, j.eps2, neg, rho, [&](int k, auto use) {
+      t.stats(j.pre, j.eps2, neg, rho, [&](int k, auto use) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) use(q, hv[k][q]);
       });
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (at.on >> k & 1u) {
-          const float4 cf = *HND_S(t.coef + t.chan(k));
+        const float4 cf = *HND_S(t.coef + t.chan(k));
 #pragma unroll
-          for (int q = 0; q < Q; ++q) hv[k][q] = fma(mul(add(hv[k][q], neg[q]), rho[q]), both(cf.z), both(cf.w));
-        }
+        for (int q = 0; q < Q; ++q) hv[k][q] = fma(mul(add(hv[k][q], neg[q]), rho[q]), both(cf.z), both(cf.w));
         t.store(at, n, k, hv[k]);
       }
     }
@@ -506,11 +531,11 @@ __global__ void __launch_bounds__(kT, 2)
                     const TT* __restrict__ dh, const TT* __restrict__ dn, TT* __restrict__ dx, TT* __restrict__ dy,
                     float4* __restrict__ part) {
   extern __shared__ __align__(16) unsigned char hnd_dyn_smem[];
-  using G = Grid<TT, K, RAG>;
+  using G = Grid<TT, K, RAG, true>;
   constexpr int Q = G::Q;
-  const G t(j, w, 4, hnd_dyn_smem);
-  const float2 inv = both(1.f / static_cast<float>(j.C));
   const int sample = blockIdx.x / chunks, stride = chunks * w;
+  const G t(j, w, 4, hnd_dyn_smem, sample);
+  const float2 inv = both(1.f / static_cast<float>(j.C));
   float4 acc[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -532,10 +557,11 @@ __global__ void __launch_bounds__(kT, 2)
     unsigned keep[K];
     float2 hv[K][Q], neg1[Q], rho1[Q], neg2[Q], rho2[Q];
     t.head(at, y != nullptr, keep, hv, neg1, rho1);
+    const bool live = at.n > 0;
     const Spot next = spot(u + stride);      // used-up slots take the next tile
     t.fetch(next, 0, x);
     if (dn) {
-      t.stats(at, j.pre, j.eps2, neg2, rho2, [&](int k, auto use) {
+      t.stats(j.pre, j.eps2, neg2, rho2, [&](int k, auto use) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) use(q, hv[k][q]);
       });
@@ -544,7 +570,6 @@ __global__ void __launch_bounds__(kT, 2)
       for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!(at.on >> k & 1u)) continue;
         const uint4 rn = t.raw(2, k);
         const float2 w2 = both((*HND_S(t.coef + t.chan(k))).z);
         float2 z = both(0.f), u = both(0.f);
@@ -557,8 +582,8 @@ __global__ void __launch_bounds__(kT, 2)
           z = fma(d, hv[k][q], z);
           u = add(u, d);
         }
-        acc[k].z += z.x + z.y;
-        acc[k].w += u.x + u.y;
+        acc[k].z += live ? z.x + z.y : 0.f;
+        acc[k].w += live ? u.x + u.y : 0.f;
       }
       t.template sum<2>(s);
 #pragma unroll
@@ -568,7 +593,6 @@ __global__ void __launch_bounds__(kT, 2)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!(at.on >> k & 1u)) continue;
         const uint4 rn = t.raw(2, k);
         uint4 rh = make_uint4(0, 0, 0, 0);
         if (dh) rh = t.raw(3, k);
@@ -581,7 +605,7 @@ __global__ void __launch_bounds__(kT, 2)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         uint4 rh = make_uint4(0, 0, 0, 0);
-        if (dh && (at.on >> k & 1u)) rh = t.raw(3, k);
+        if (dh) rh = t.raw(3, k);
 #pragma unroll
         for (int q = 0; q < Q; ++q) hv[k][q] = Vec<TT>::get(rh, q);
       }
@@ -597,26 +621,22 @@ __global__ void __launch_bounds__(kT, 2)
       for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!(at.on >> k & 1u)) continue;
         const uint4 ry = t.raw(1, k);
         const float2 al = both((*HND_S(t.coef + t.chan(k))).x * t.gate(at, k));
+        const unsigned bits = j.border ? keep[k] : ~0u;
         float2 a = both(0.f), r = both(0.f);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
           const float2 yh = mul(add(Vec<TT>::get(ry, q), neg1[q]), rho1[q]);
-          float2 md = mul(hv[k][q], both(j.factor));
-          if (j.border) {
-            md.x = (keep[k] >> (2 * q) & 1u) ? md.x : 0.f;
-            md.y = (keep[k] >> (2 * q + 1) & 1u) ? md.y : 0.f;
-          }
+          const float2 md = G::kept(bits, q, mul(hv[k][q], both(j.factor)));
           a = fma(md, yh, a);
           r = add(r, md);
           hv[k][q] = mul(md, al);      // e from here on
           s[0][q] = add(s[0][q], hv[k][q]);
           s[1][q] = fma(hv[k][q], yh, s[1][q]);
         }
-        acc[k].x += a.x + a.y;
-        acc[k].y += r.x + r.y;
+        acc[k].x += live ? a.x + a.y : 0.f;
+        acc[k].y += live ? r.x + r.y : 0.f;
       }
       if (j.post) {
         t.template sum<2>(s);
@@ -628,7 +648,7 @@ __global__ void __launch_bounds__(kT, 2)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (j.post && (at.on >> k & 1u)) {
+        if (j.post) {
           const uint4 ry = t.raw(1, k);
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
@@ -652,7 +672,7 @@ __global__ void __launch_bounds__(kT, 2)
       s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
       s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, o);
     }
-    if ((t.chans >> k & 1u) && t.lane == 0) *HND_G(part + blockIdx.x * j.C + t.chan(k)) = s;
+    if (t.there(k) && t.lane == 0) *HND_G(part + blockIdx.x * j.C + t.chan(k)) = s;
   }
 }
 

@@ -267,11 +267,6 @@ static JoinDev device_view(const JoinArgs& a) {
 
 // ------------------------------------------------------------------ launches
 static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-static int pow2_up(long long v) {
-  int p = 1;
-  while (p < v) p *= 2;
-  return p;
-}
 
 // How a call runs; a function of the shape alone.
 struct JoinPlan {
@@ -363,7 +358,7 @@ static JoinPlan join_plan(long long B, long long C, long long L, int bf16, bool 
     if (backward)
       p.K = p.V == 1 ? 8 : 4;
     else
-      p.K = p.V == 1 ? (C <= 256 ? 8 : 32) : 32 / wide;
+      p.K = p.V == 1 ? 32 : 32 / wide;
     if (!grid_plan(p, C, units, p.V == 1 ? 32 : 8)) return p;
     if (backward) {
       const long long tiles = cdiv(per, p.lanes), want = cdiv(kJoinParts, B);
@@ -414,13 +409,24 @@ static cudaError_t forward(const JoinArgs& a) {
     if (p.V == 1) return p.K == 1 ? forward_as<TT, 1, 1, true>(a, p) : forward_as<TT, 1, 16, true>(a, p);
     return p.K == 1 ? forward_as<TT, W, 1, true>(a, p) : forward_as<TT, W, 32 / W, true>(a, p);
   }
-  if (p.V == 1) return p.K == 8 ? forward_as<TT, 1, 8, false>(a, p) : forward_as<TT, 1, 32, false>(a, p);
-  return forward_as<TT, W, 32 / W, false>(a, p);
+  return p.V == 1 ? forward_as<TT, 1, 32, false>(a, p) : forward_as<TT, W, 32 / W, false>(a, p);
 }
 
 // The parameters' gradients from `rows` rows of sums, `per` a sample.
 static cudaError_t grads(const JoinArgs& a, const float4* part, long long rows, long long per) {
   const long long wide = cdiv(a.C, 32);
+  // the checked build's table has no room for these next to the activations
+  const size_t C4 = 4 * static_cast<size_t>(a.C), BC4 = C4 * static_cast<size_t>(a.B);
+  BoundsList bl;
+  bl.add(part, static_cast<size_t>(rows) * a.C * sizeof(float4));
+  for (const float* p : {a.post.w, a.post.b, a.scale, static_cast<const float*>(a.dpost_w),
+                         static_cast<const float*>(a.dpost_b), static_cast<const float*>(a.dscale),
+                         static_cast<const float*>(a.dpre_w), static_cast<const float*>(a.dpre_b)})
+    bl.add(p, C4);
+  bl.add(a.gate, BC4);
+  bl.add(a.dgate, BC4);
+  const cudaError_t e = bounds_register(bl, nullptr, a.stream);
+  if (e != cudaSuccess) return e;
   k_join_grads<<<static_cast<unsigned>(wide * (a.dgate && per ? 1 + a.B : 1)), dim3(32, 32), 0, a.stream>>>(
       device_view(a), part, rows, per, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});
   return cudaGetLastError();

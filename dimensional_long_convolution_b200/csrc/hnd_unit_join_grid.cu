@@ -15,7 +15,7 @@ static long long row_vectors(const JoinArgs& a) {
 template <class TT, int K, bool RAG>
 static cudaError_t fwd(const JoinArgs& a, const JoinDev& j, int w, unsigned blocks) {
   auto kern = grid::k_join_grid_fwd<TT, K, RAG>;
-  const size_t smem = grid::smem_bytes(2, K, a.C, w, 16 / sizeof(TT), RAG);
+  const size_t smem = grid::smem_bytes(2, K, w, 16 / sizeof(TT), RAG);
   const cudaError_t e = ensure_smem(kern, kGridSmem);
   if (e != cudaSuccess) return e;
   const long long per = RAG ? (row_vectors(a) + w - 1) / w : row_vectors(a);
@@ -28,7 +28,7 @@ static cudaError_t fwd(const JoinArgs& a, const JoinDev& j, int w, unsigned bloc
 template <class TT, int K, bool RAG>
 static cudaError_t bwd(const JoinArgs& a, const JoinDev& j, int w, int chunks, unsigned blocks, float4* part) {
   auto kern = grid::k_join_grid_bwd<TT, K, RAG>;
-  const size_t smem = grid::smem_bytes(4, K, a.C, w, 16 / sizeof(TT), RAG);
+  const size_t smem = grid::smem_bytes(4, K, w, 16 / sizeof(TT), RAG);
   const cudaError_t e = ensure_smem(kern, kGridSmem);
   if (e != cudaSuccess) return e;
   kern<<<blocks, grid::kT, smem, a.stream>>>(j, w, static_cast<int>(row_vectors(a)), chunks,

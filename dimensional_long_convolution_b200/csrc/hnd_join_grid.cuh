@@ -59,6 +59,7 @@ template <class TT>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
+  using Bits = unsigned short;
   static constexpr int Q = 4;
   static __device__ __forceinline__ float2 get(const uint4& u, int q) {
     const uint32_t w = q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w;
@@ -76,6 +77,7 @@ struct Vec<__nv_bfloat16> {
 };
 template <>
 struct Vec<float> {
+  using Bits = unsigned;
   static constexpr int Q = 2;
   static __device__ __forceinline__ float2 get(const uint4& u, int q) {
     return q == 0 ? make_float2(__uint_as_float(u.x), __uint_as_float(u.y))
@@ -142,21 +144,22 @@ __device__ __forceinline__ void put_some(TT* p, const uint4& a, unsigned bits) {
 }
 
 // Shared memory: slots [tensor][K][rows][w, and one more if ragged] of 16
-// bytes, factors [K][rows], sums.
+// bytes, factors [K][rows], sums; ragged: [2][rows][2] vectors of row ends.
 inline size_t smem_bytes(int tensors, int K, int w, int V, bool ragged) {
-  return static_cast<size_t>(tensors) * K * (kT + (ragged ? kT / w : 0)) * 16 + static_cast<size_t>(K) * (kT / w) * 16 +
-         sizeof(float) * (kWarps + 1) * 2 * w * V;
+  const size_t rows = kT / w, slots = static_cast<size_t>(tensors) * K * (kT + (ragged ? rows : 0));
+  return 16 * (slots + K * rows + (ragged ? 4 * rows : 0)) + sizeof(float) * (kWarps + 1) * 2 * w * V;
 }
 
 // Where a thread's vectors of a tile lie: its first element, its sample, a bit
 // for each of its channels that is there, and how many of its positions are
-// (ragged: and whether the next lane has some).
+// (ragged: whether the next lane has some, and whether all of the tile's are
+// there).
 struct Spot {
   long long at;
   int b;
   unsigned on;
   int n;
-  bool next;
+  bool next, inner;
 };
 
 // FIX: the block keeps to one sample, whose gate goes into the factors.
@@ -173,6 +176,8 @@ struct Grid {
   DropState ds{};
   float* part;                      // [kWarps][2 V w]
   float* total;                     // [2 V w]
+  uint4* ends;                      // ragged: of the thread's row, its first and last lane's vector, in turns
+  mutable int turn = 0;
 
   __device__ Grid(const JoinDev& jj, int lanes, int tensors, unsigned char* smem, long long sample)
       : j(jj), w(lanes), lane(threadIdx.x % lanes), cg(threadIdx.x / lanes), rows(kT / lanes), C(static_cast<int>(jj.C)) {
@@ -185,6 +190,7 @@ struct Grid {
     coef = reinterpret_cast<float4*>(reinterpret_cast<uint4*>(smem) + tensors * K * pitch);
     part = reinterpret_cast<float*>(coef + K * rows);
     total = part + kWarps * 2 * V * w;
+    ends = reinterpret_cast<uint4*>(total + 2 * V * w) + 2 * cg;
     for (int c = threadIdx.x; c < K * rows; c += kT) {
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < C) {
@@ -220,7 +226,7 @@ struct Grid {
   __device__ Spot spot(int b, int u, int left) const {
     const bool live = left > 0;
     return Spot{b * j.C * j.L + static_cast<long long>(u) * V + own, live ? b : 0, live ? chans : 0u,
-                live ? min(left, V) : 0, RAG && lane + 1 < w && left > V};
+                live ? min(left, V) : 0, RAG && lane + 1 < w && left > V, RAG && left >= (w - lane) * V};
   }
   __device__ void fetch(const Spot& s, int tensor, const TT* p) const {
     if (!p) return;
@@ -276,6 +282,23 @@ struct Grid {
       // the vector that the lane's first position lies in, and what spills into the one after it
       const uint4 head = at ? funnel<TT>(before, mine, V - at) : mine;
       TT* to = p + (e - at);
+      if (s.inner) {
+        // Whole vectors, but for a row's first and last, which lie in V elements of its first and last lane: element
+        // i of the one or the other, by lane i.
+        uint4* pair = ends + turn * 2 * rows;      // two turns: the one before last has been read
+        turn ^= 1;
+        if (lane == 0) *HND_S(pair) = mine;
+        if (lane == w - 1) *HND_S(pair + 1) = mine;
+        __syncwarp();
+        if (on && (lane || !at)) __stcs(HND_G(reinterpret_cast<uint4*>(to)), head);
+        using Bits = typename Vec<TT>::Bits;
+        for (int i = lane; i < V; i += w) {
+          const int last = i >= V - at;
+          const Bits v = *HND_S(reinterpret_cast<const Bits*>(pair + last) + i);
+          if (on && at) *HND_G(reinterpret_cast<Bits*>(p + (e - lane * V + last * (w - 1) * V + i))) = v;
+        }
+        return;
+      }
       unsigned some = on ? (2u << min(V, at + s.n) - 1) - (lane ? 1u : 1u << at) : 0u;
       if (some == (1u << V) - 1) {
         __stcs(HND_G(reinterpret_cast<uint4*>(to)), head);

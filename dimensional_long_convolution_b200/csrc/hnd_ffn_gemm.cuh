@@ -80,8 +80,8 @@ struct Job {
   long long M, N;            // extents of D
   int cols;                  // columns of a tile of kEpiOut: 256, 128 or 64
   int kind, map;             // how D leaves, and the map of kOutTma
-  void* ptr;                 // D otherwise: element (m, n) of split s at
-  long long bs, rs;          //   s bs + n rs + m, or with group > 0 at
+  void* ptr;                 // D otherwise: element (m, n) of split s and batch b at
+  long long bs, rs;          //   (s batches + b) bs + n rs + m, or with group > 0 at
   long long group, gs;       //   (m / group) gs + n rs + m % group; kOutTok: m rs + n
 };
 
@@ -387,6 +387,16 @@ __device__ __forceinline__ void with_act(int act, Fn fn) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 bytes in one store: a whole sector of memory, which two of 16 are not.
+struct alignas(32) Vec32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(HND_G(reinterpret_cast<Vec32*>(p))),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void stage_put(uint32_t addr, float v) {
@@ -739,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
             if (c + 32 == per) release();
             if (n0 >= j.N) continue;
             if (j.kind == kOutF32) {
-              float* o = static_cast<float*>(j.ptr) + (j.splits > 1 ? ti.split * j.bs : 0) + at;
+              float* o = static_cast<float*>(j.ptr) + (static_cast<long long>(ti.split) * j.batches + ti.batch) * j.bs + at;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __uint_as_float(v[i]);
@@ -767,10 +777,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
             with_act(p.act, [&](auto kind) {
               constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-              for (int i0 = 0; i0 < 32; i0 += 8) {
-                uint32_t w[3][4];
+              for (int i0 = 0; i0 < 32; i0 += 16) {
+                uint32_t w[3][8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 8; ++i) {
                   const int at = i0 + 2 * i;
                   const float gv[2] = {__uint_as_float(g[at]), __uint_as_float(g[at + 1])};
                   const float uv[2] = {__uint_as_float(u[at]), __uint_as_float(u[at + 1])};
@@ -780,9 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
                 }
                 if (live && n0 + i0 < j.N)
 #pragma unroll
-                  for (int k = 0; k < 3; ++k)
-                    *HND_G(reinterpret_cast<uint4*>(o + k * p.hid_plane + i0)) =
-                        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                  for (int k = 0; k < 3; ++k) store32(o + k * p.hid_plane + i0, w[k]);
               }
             });
           }
@@ -830,16 +838,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int i0 = 0; i0 < W; i0 += 8) {
-            uint32_t w[3][4];
+          for (int i0 = 0; i0 < W; i0 += 16) {
+            uint32_t w[3][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
               split3x2(sum[q][i0 + 2 * i], sum[q][i0 + 2 * i + 1], w[0][i], w[1][i], w[2][i]);
             if (live && n0 + i0 < j.N)
 #pragma unroll
-              for (int k = 0; k < 3; ++k)
-                *HND_G(reinterpret_cast<uint4*>(o + apart[q] + k * p.hid_plane + i0)) =
-                    make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+              for (int k = 0; k < 3; ++k) store32(o + apart[q] + k * p.hid_plane + i0, w[k]);
           }
       } else {
         if constexpr (EPI == kEpiOut) {
@@ -873,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
               for (int i = 0; i < 32; ++i)
                 if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __float2bfloat16_rn(__uint_as_float(v[i]));
             } else if (j.kind == kOutF32) {
-              float* o = static_cast<float*>(j.ptr) + ti.split * j.bs + m;      // a split's part of a weight gradient
+              float* o = static_cast<float*>(j.ptr) + (static_cast<long long>(ti.split) * j.batches + ti.batch) * j.bs + m;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (live && n0 + i < j.N) *HND_G(o + (n0 + i) * j.rs) = __uint_as_float(v[i]);

@@ -91,6 +91,26 @@ __global__ void __launch_bounds__(256) k_ffn_sum(const float* __restrict__ parts
   }
 }
 
+// Sums of the partial products [split][batch][C][Lx] of y or dx, back into the
+// activations' layout: element (batch, c, m) of token-major positions at
+// m C + c, else at (t / L) C L + c L + t % L with t the position in all.
+template <class TT>
+__global__ void __launch_bounds__(256)
+    k_ffn_fold(const float* __restrict__ parts, TT* __restrict__ out, long long C, long long L, long long Lx, long long n,
+               int splits, int token) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    float s = 0.f;
+    for (int k = 0; k < splits; ++k) s += *HND_G(parts + k * n + i);
+    const long long row = i / Lx, m = i - row * Lx, b = row / C, c = row - b * C;
+    if (token) {
+      st1(out + m * C + c, s);
+    } else {
+      const long long t = b * Lx + m, sample = t / L;
+      st1(out + (sample * C + c) * L + (t - sample * L), s);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- planning
 static long long up(long long v, long long a) { return (v + a - 1) / a * a; }
 static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -105,9 +125,10 @@ struct Layout {
   long long batches, Lx;     // of the position axis as the products see it
   long long pitch;           // of packed rows (token: of a position's channels)
   long long hpitch;          // of a position's hidden channels
-  size_t x, dy, w, hid, part, bytes;
+  size_t x, dy, w, hid, part, fold, bytes;
   long long act_plane, w_plane, hid_plane;   // elements
-  int splits;
+  int splits;                // of the weight gradients
+  int cols, folds;           // of y and dx: columns of a tile, splits
 };
 
 // Columns of the tiles of a product of `N` columns over `m_tiles` tiles of 256
@@ -119,6 +140,17 @@ static int tile_cols(long long N, long long m_tiles) {
   int cols = 256;
   while (cols > 64 && (N <= cols / 2 || m_tiles * cdiv(N, cols) < kPairs / 2)) cols /= 2;
   return cols;
+}
+
+// Splits of the K loop of y or dx, where there are so few tiles that most
+// pairs would be idle, each of eight stages at least: the partial sums are
+// those of 74 tiles at most (9 positions, C 24, F 5280, fp32 training: one
+// tile of 1000 stages, 310 us unsplit).
+static int data_splits(long long tiles, long long stages) {
+  const long long most = kPairs / tiles, deep = stages / 8;
+  long long s = most < deep ? most : deep;
+  if (s < 2) return 1;
+  return static_cast<int>(cdiv(stages, cdiv(stages, s)));
 }
 
 // Splits of the weight gradients' K loops.  In stages of a pair (0.27 us at
@@ -151,7 +183,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   l.batches = merged ? 1 : a.B;
   l.Lx = merged ? T : a.L;
   l.pitch = l.token ? a.C : up(T, 8);
-  l.hpitch = a.F;
+  l.hpitch = a.bf16 ? a.F : up(a.F, 16);      // fp32: whole 32-byte stores
   const bool copied = l.packed || !a.bf16;
   size_t at = 0;
   auto take = [&](long long elements, size_t size) {
@@ -174,6 +206,9 @@ static Layout layout(const FfnArgs& a, bool backward) {
   if (copied && backward) l.dy = take(l.planes * l.act_plane, 2);
   if (!a.bf16) l.w = take(9 * l.w_plane, 2);
   l.hid = take((backward ? 3 : 1) * l.planes * l.hid_plane, 2);
+  l.cols = tile_cols(a.C, l.batches * cdiv(l.Lx, 256));
+  l.folds = data_splits(l.batches * cdiv(l.Lx, 256) * cdiv(a.C, l.cols), cdiv(a.F, kBK));
+  if (l.folds > 1) l.fold = take(l.folds * l.batches * a.C * l.Lx, 4);
   l.splits = 1;
   if (backward) {
     // every split gets a stage at least
@@ -423,6 +458,15 @@ struct Ffn {
   // y or dx: back to the activations' own layout
   void activation_out(Launch& n, Job& j, void* p) const {
     j.ptr = p;
+    if (l.folds > 1) {
+      j.splits = l.folds;
+      j.kper = static_cast<int>(cdiv(j.kblocks, l.folds));
+      j.kind = kOutF32;
+      j.ptr = ws(l.fold);
+      j.rs = l.Lx;
+      j.bs = a.C * l.Lx;
+      return;
+    }
     if (l.token) {
       j.kind = kOutTok;
       j.rs = a.C;
@@ -437,6 +481,14 @@ struct Ffn {
     }
   }
 
+  cudaError_t fold(void* out) const {
+    if (l.folds == 1) return cudaSuccess;
+    const long long n = l.batches * a.C * l.Lx, blocks = cdiv(n, 256);
+    k_ffn_fold<TT><<<static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, a.stream>>>(
+        reinterpret_cast<const float*>(ws(l.fold)), static_cast<TT*>(out), a.C, a.L, l.Lx, n, l.folds, l.token);
+    return cudaGetLastError();
+  }
+
   cudaError_t forward() const {
     cudaError_t e;
     if ((e = pack(false)) != cudaSuccess) return e;
@@ -446,12 +498,13 @@ struct Ffn {
     h.job(data_job(1, a.F, hn, a.C));
     if ((e = run<kEpiHidden, F32>(h, a.stream)) != cudaSuccess) return e;
     Launch y = start();
-    const int on = tile_cols(a.C, l.batches * cdiv(l.Lx, 256));
+    const int on = l.cols;
     y.p.seg[0] = data_seg(y.km(hid[0]), y.km(wd, on / 2), false, false, on, 0, 1);
     Job j = data_job(1, a.C, on, a.F);
     activation_out(y, j, a.y);
     y.job(j);
-    return run<kEpiOut, F32>(y, a.stream);
+    e = run<kEpiOut, F32>(y, a.stream);
+    return e == cudaSuccess ? fold(a.y) : e;
   }
 
   cudaError_t backward() const {
@@ -473,13 +526,13 @@ struct Ffn {
     // dX
     Launch d = start();
     d.p.piece = 2;      // of both its segments
-    const int on = tile_cols(a.C, l.batches * cdiv(l.Lx, 256));
+    const int on = l.cols;
     d.p.seg[0] = data_seg(d.km(hid[1]), d.mn(wg), false, true, on, 0, 1);
     d.p.seg[1] = data_seg(d.km(hid[2]), d.mn(wu), false, true, on, 0, 0);
     Job j = data_job(2, a.C, on, a.F);
     activation_out(d, j, a.dx);
     d.job(j);
-    if ((e = run<kEpiOut, F32>(d, a.stream)) != cudaSuccess) return e;
+    if ((e = run<kEpiOut, F32>(d, a.stream)) != cudaSuccess || (e = fold(a.dx)) != cudaSuccess) return e;
     // dWg[f][c] = dG X', dWu[f][c] = dU X', dWd[c][f] = dY H'
     Launch w = start();
     const bool batched = l.batches > 1;

@@ -430,6 +430,11 @@ FFN = [
     ((16, 16, 16), 1, 64, 256, "f32", "gelu"),
     ((64, 32), 2, 512, 640, "bf16", "silu"),
     ((2056,), 1, 8, 1032, "bf16", "silu"),        # few channels, many hidden
+    ((1,), 40, 24, 2088, "f32", "silu"),          # few tiles, long sums: their depth is split
+    ((1,), 40, 72, 2088, "bf16", "gelu"),
+    ((50,), 2, 64, 2056, "bf16", "silu"),
+    ((256,), 2, 40, 2560, "bf16", "silu"),
+    ((30,), 3, 40, 1112, "f32", "gelu"),
     ((72,), 2, 1032, 8, "bf16", "gelu"),
 ]
 

@@ -487,15 +487,17 @@ struct Plan {
   // have fewer: a thread holds its columns' sums in registers
   static constexpr int kCols = EPI == kEpiHidden ? 128 : F32 && EPI == kEpiGrad ? 64 : 256;
   static constexpr int kOuts = EPI == kEpiGrad ? 3 : 1;
-  // Four warps of epilogue see all lanes; two such groups share the columns.
-  static constexpr int kGroups = 2;
+  // Four warps of epilogue see all lanes; two such groups share the columns,
+  // or four where little else runs under them (bf16 gradients).
+  static constexpr int kGroups = EPI == kEpiGrad && !F32 ? 4 : 2;
   static constexpr int kThreads = 32 * (3 + 4 * kGroups);           // a warp for A's copies, one for the MMAs, one for B's
   // bf16 leaves by TMA, gathered in shared memory: of each group and output
-  // 128 positions x kWide hidden channels, or (kEpiOut) 32 n x 128 m; twice,
-  // so that a copy out runs under the next one's gathering
+  // 128 positions x kWide hidden channels, or (kEpiOut) 32 n x 128 m; where
+  // there is room twice, so that a copy out runs under the next gathering
   static constexpr int kWide = EPI == kEpiGrad ? 32 : 64;
   static constexpr int kStoreBytes = EPI == kEpiOut ? 8192 : 256 * kWide;
-  static constexpr int kGroupStore = F32 ? 0 : 2 * kOuts * kStoreBytes;
+  static constexpr int kStoreBufs = EPI == kEpiGrad ? 1 : 2;
+  static constexpr int kGroupStore = F32 ? 0 : kStoreBufs * kOuts * kStoreBytes;
   static constexpr int kStages = F32 ? 7 : EPI == kEpiGrad ? 4 : EPI == kEpiHidden ? 5 : 6;
   static constexpr int kSmem = 1024 + kStages * kStage + kGroups * kGroupStore + 8 * (2 * kStages + 2 * kBufs) + 16;
 };
@@ -897,45 +899,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
             }
           }
         } else {
-          // a turn's 128 hidden channels: 64 of each group, 16 at a time, gathered as rows of kWide channels of a
+          // a turn's 128 hidden channels: 64 or 32 of each group, 16 at a time, gathered as rows of kWide channels of a
           // position (a thread's own 32-byte stores leave an SM at 16 bytes a cycle: 90 us for the gradients at C
           // 256, F 1024, 32768 positions)
-          constexpr int W = 16, kPer = PL::kWide / W, kChunks = PL::kWide / 8;
+          constexpr int W = 16, kPer = PL::kWide / W, kChunks = PL::kWide / 8, kMine = 128 / GR;
+          constexpr int kAhead = GR == 2 ? 1 : 0;      // four groups hide their latencies by turns, and have no registers
           bool yes = true;
           for (int turn = 0; turn < PL::kTurns; ++turn) {
             const int n0 = ti.nt * PL::kCols + turn * 128;
             if (n0 >= j.N || !(yes = arrived())) break;
-            const uint32_t acc = tmem + lanes + buf * 256 + group * 64;
+            const uint32_t acc = tmem + lanes + buf * 256 + group * kMine;
             // the next 16 channels are on their way while these are worked on
-            uint32_t g[2][W], u[2][W], d[2][EPI == kEpiGrad ? W : 1];
+            uint32_t g[kAhead + 1][W], u[kAhead + 1][W], d[kAhead + 1][EPI == kEpiGrad ? W : 1];
             auto load = [&](int c) {
-              tmem_load(g[c & 1], acc + c * W);
-              tmem_load(u[c & 1], acc + 128 + c * W);
-              if constexpr (EPI == kEpiGrad) tmem_load(d[c & 1], acc + 256 + turn * 128 + c * W);
+              tmem_load(g[c & kAhead], acc + c * W);
+              tmem_load(u[c & kAhead], acc + 128 + c * W);
+              if constexpr (EPI == kEpiGrad) tmem_load(d[c & kAhead], acc + 256 + turn * 128 + c * W);
             };
             load(0);
             with_act(p.act, [&](auto kind) {
               constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-              for (int c = 0; c < 64 / W; ++c) {
+              for (int c = 0; c < kMine / W; ++c) {
+                if (!kAhead && c) load(c);
                 tmem_wait_load();
-                if (c + 1 < 64 / W)
-                  load(c + 1);
-                else
-                  release();
+                if (kAhead && c + 1 < kMine / W) load(c + 1);
+                if (c + 1 == kMine / W) release();
                 const uint32_t to = stage + sbuf * (PL::kOuts * PL::kStoreBytes);
                 if (c % kPer == 0) {      // this buffer's copies before the last have left it
-                  if (issuer) store_wait_read<1>();
+                  if (issuer) store_wait_read<PL::kStoreBufs - 1>();
                   named_sync(1 + group, 128);
                 }
                 uint32_t w[PL::kOuts][8];
 #pragma unroll
                 for (int i = 0; i < W; i += 2) {
-                  const float gv[2] = {__uint_as_float(g[c & 1][i]), __uint_as_float(g[c & 1][i + 1])};
-                  const float uv[2] = {__uint_as_float(u[c & 1][i]), __uint_as_float(u[c & 1][i + 1])};
+                  const float gv[2] = {__uint_as_float(g[c & kAhead][i]), __uint_as_float(g[c & kAhead][i + 1])};
+                  const float uv[2] = {__uint_as_float(u[c & kAhead][i]), __uint_as_float(u[c & kAhead][i + 1])};
                   float r[3][2];
                   if constexpr (EPI == kEpiGrad) {
-                    const float dv[2] = {__uint_as_float(d[c & 1][i]), __uint_as_float(d[c & 1][i + 1])};
+                    const float dv[2] = {__uint_as_float(d[c & kAhead][i]), __uint_as_float(d[c & kAhead][i + 1])};
                     hidden_grads2<false, ACT>(gv, uv, dv, r[0], r[1], r[2]);
                   } else {
                     hidden2<false, ACT>(gv, uv, r[0]);
@@ -958,14 +960,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<EPI, F32>::kThr
                   fence_async();
                   named_sync(1 + group, 128);
                   if (issuer) {
-                    const int n = n0 + group * 64 + c / kPer * PL::kWide;
+                    const int n = n0 + group * kMine + c / kPer * PL::kWide;
                     if (m0 < j.M && n < j.N)
 #pragma unroll
                       for (int q = 0; q < PL::kOuts; ++q)
                         tma_store(&p.map[p.hmap[q]], to + q * PL::kStoreBytes, n, m0, ti.batch);
                     store_commit();
                   }
-                  sbuf ^= 1;
+                  sbuf = (sbuf + 1) % PL::kStoreBufs;
                 }
               }
             });

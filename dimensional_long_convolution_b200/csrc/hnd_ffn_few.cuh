@@ -11,8 +11,8 @@
 // order, the fragments' k are simply these (weights and positions alike).
 // The warps' sums meet in shared memory.
 //
-// C 2048, F 5632, 4 positions, bf16 (69 MB of weights): XX us, 62 us with the
-// large tiles.
+// C 2048, F 5632, 4 positions, bf16 (69 MB of weights): 19.8 us a pass, 62 us
+// with the large tiles.
 #pragma once
 
 #include <cuda_bf16.h>

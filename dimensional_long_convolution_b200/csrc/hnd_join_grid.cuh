@@ -22,7 +22,10 @@
 // the lane before, so that all but a row's first and last vector leave whole.
 // Eight elements then take two counters of the generator; the second is the
 // next lane's first.  (One value a thread and load, as hnd_join.cuh does it for
-// such rows, took 107 us for 13 x 204 x 777 bf16 forward and backward.)
+// such rows, took 107 us for 13 x 204 x 777 bf16 forward and backward, this 90.)
+//
+// 2 x 128 x 256^2 bf16 forward: 31 us.  8 x 256 x 64^2 fp32: forward 31 us,
+// backward 67, bound by instruction issue and latency (51 and 42% of the slots).
 #pragma once
 
 #include "hnd_div.cuh"

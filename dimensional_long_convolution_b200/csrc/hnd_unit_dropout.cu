@@ -4,7 +4,8 @@
 // Bound by memory (two bytes moved a byte of activations) as long as the ten
 // rounds, some 60 integer operations for eight elements, stay hidden behind
 // it: a thread takes eight elements, one counter, as one or two 16-byte
-// loads, four groups in flight.
+// loads, four groups in flight.  32 x 128^3 bf16: 53 us, 77% of the rate of a
+// copy.
 #include "hnd_block.h"
 #include "hnd_io.cuh"
 #include "hnd_philox.cuh"

@@ -132,10 +132,10 @@ struct Layout {
 };
 
 // Columns of the tiles of a product of `N` columns over `m_tiles` tiles of 256
-// rows: 256, unless there are fewer, or fewer tiles than half the pairs. An
-// MMA takes as long for 64 columns as for 256, so narrower tiles only pay
+// rows: 256, unless there are fewer, or fewer tiles than half the pairs.
+// Narrower tiles bring the rows of A in more often, so they are only taken
 // where pairs would be idle (3 x 777 positions, C 200, F 536: 10 tiles, the
-// second product 13 us with 256 columns, 10 with 64).
+// second product 13 us with 256 columns, 9.3 with 64).
 static int tile_cols(long long N, long long m_tiles) {
   int cols = 256;
   while (cols > 64 && (N <= cols / 2 || m_tiles * cdiv(N, cols) < kPairs / 2)) cols /= 2;
@@ -145,7 +145,7 @@ static int tile_cols(long long N, long long m_tiles) {
 // Splits of the K loop of y or dx, where there are so few tiles that most
 // pairs would be idle, each of eight stages at least: the partial sums are
 // those of 74 tiles at most (9 positions, C 24, F 5280, fp32 training: one
-// tile of 1000 stages, 310 us unsplit).
+// tile of 1000 stages, training 310 us unsplit, 118 so).
 static int data_splits(long long tiles, long long stages) {
   const long long most = kPairs / tiles, deep = stages / 8;
   long long s = most < deep ? most : deep;

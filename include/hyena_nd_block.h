@@ -127,7 +127,10 @@ HYENA_ND_API hyena_nd_status hyena_nd_dropout(const hyena_nd_block_shape* s, dou
 /* The gated feed-forward block.  act: the gate's activation, SILU
  * g / (1 + exp(-g)) or GELU g Phi(g) (the normal distribution function).
  * Weights in the activations' dtype, row-major: Wg, Wu [F, C], Wd [C, F].
- * C and F: multiples of 8 up to 65536 (else HYENA_ND_ERR_UNSUPPORTED). */
+ * C and F: multiples of 8 up to 65536 (else HYENA_ND_ERR_UNSUPPORTED).
+ * With bf16 the hidden values act(g) u, and in the gradients those of g and u
+ * too, are rounded to bf16 once before the next product.  With fp32 an
+ * infinity in an operand gives NaN in what it reaches. */
 typedef enum { HYENA_ND_ACT_SILU = 0, HYENA_ND_ACT_GELU = 1 } hyena_nd_act;
 
 typedef struct {

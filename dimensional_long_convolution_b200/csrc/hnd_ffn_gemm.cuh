@@ -307,20 +307,21 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // 1 / (1 + exp(-g)) of two gates.  bf16: one reciprocal of the product serves
 // both, since the special-function unit (two exponentials and two reciprocals
 // for a pair otherwise) is what the epilogue waits for; exp(-g) is held at
-// 2^60 to keep the product finite, so that gates below -41.6 get 2^-60 for
-// their smaller value.
+// 2^60 to keep the product finite, and gates beyond that (-41.6) get 0, since
+// what is small next to 1 is not small once a large gate multiplies it.  fp32:
+// the reciprocal of an infinite exponential is 0 by itself.
 template <bool F32>
 __device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
   if constexpr (F32) {
-    s[0] = recip_fast(1.f + expf(fminf(-g[0], 87.f)));     // off by one unit in the last place at most
-    s[1] = recip_fast(1.f + expf(fminf(-g[1], 87.f)));
+    s[0] = recip_fast(1.f + expf(-g[0]));     // off by one unit in the last place at most
+    s[1] = recip_fast(1.f + expf(-g[1]));
   } else {
     float x[2];
     unpair(mul2(pair64(g[0], g[1]), pair64(-kLog2e, -kLog2e)), x);
     const float d0 = 1.f + exp2_fast(fminf(x[0], 60.f)), d1 = 1.f + exp2_fast(fminf(x[1], 60.f));
     const float r = recip_fast(d0 * d1);
-    s[0] = r * d1;
-    s[1] = r * d0;
+    s[0] = x[0] > 60.f ? 0.f : r * d1;
+    s[1] = x[1] > 60.f ? 0.f : r * d0;
   }
 }
 

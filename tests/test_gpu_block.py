@@ -462,6 +462,32 @@ def test_ffn_extreme_gates(dt):
         c.check()
 
 
+@pytest.mark.parametrize("gate", [1e3, 1e15, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("dims,dt", [((1,), "bf16"), ((40,), "bf16"), ((1,), "f32"), ((40,), "f32")])
+def test_ffn_gates_of_any_size(dims, dt, gate):
+    """silu(g) and its slope are 0 at g = -gate (below 1e-400), however large the gate: the sigmoid has to be 0
+    there, not small, since g multiplies it.  Every other hidden channel has g = 0, act 0 and slope 1/2, so that
+    only dwg has values: its odd rows, (sum of wd) / 2 at each position.  All of them are exact in bf16; fp32's
+    reciprocal is off by 2^-22 at most."""
+    C = F = 8
+    L = int(np.prod(dims))
+    x = np.zeros((1, C) + dims)
+    x[:, 0] = 1
+    wg, wu, wd = np.zeros((F, C)), np.zeros((F, C)), np.ones((C, F))
+    wg[::2, 0] = -gate
+    wu[:, 0] = 1
+    x, wg, wu, wd, dy = (dev(v, dt) for v in (x, wg, wu, wd, np.ones((1, C) + dims)))
+    op = K.GatedFFN(dims, 1, C, F, io_dtype=dt, act="silu")
+    y = op(x, wg, wu, wd)
+    dx, dwg, dwu, dwd = (host(v) for v in op.backward(x, wg, wu, wd, dy))
+    assert op.status() == H.OK
+    want = np.zeros((F, C))
+    want[1::2, 0] = C / 2 * L
+    for name, got in (("y", host(y)), ("dx", dx), ("dwu", dwu), ("dwd", dwd)):
+        assert (got == 0).all(), (name, np.abs(got).max())
+    assert (np.abs(dwg - want) <= 2.0 ** -22 * want).all()
+
+
 @pytest.mark.parametrize("dims", [(1,), (40,), (7,)])
 def test_ffn_nan_stays_in_its_position(dims):
     c = FfnCase(dims, 3, 64, 96, "bf16", "silu")

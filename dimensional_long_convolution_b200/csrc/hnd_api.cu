@@ -64,7 +64,7 @@ cudaError_t side_stream(SideStream** out) {
 
 #ifdef HYENA_ND_BOUNDS
 __device__ BoundsTable g_bounds;
-__device__ __align__(16) unsigned char g_bounds_dummy[256];
+__device__ __align__(32) unsigned char g_bounds_dummy[256];
 
 cudaError_t bounds_register(const BoundsList& l, int* status, cudaStream_t st) {
   BoundsTable t{};

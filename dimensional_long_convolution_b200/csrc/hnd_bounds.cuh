@@ -35,7 +35,7 @@ struct BoundsTable {
 // One table for the whole library (relocatable device code), written by the
 // host at the start of every call (stream-ordered).
 extern __device__ BoundsTable g_bounds;
-extern __device__ __align__(16) unsigned char g_bounds_dummy[256];
+extern __device__ __align__(32) unsigned char g_bounds_dummy[256];      // the widest access: 32 bytes
 
 __device__ __forceinline__ bool bounds_ok(const void* p, size_t nbytes) {
   if (__isShared(p)) {

@@ -397,6 +397,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // 32 bytes in one store: a whole sector of memory, which two of 16 are not.
+// p on 32 bytes.
 struct alignas(32) Vec32 {
   uint32_t w[8];
 };

@@ -117,6 +117,10 @@ static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 constexpr int kPairs = 74;   // CTA pairs of a B200
 
+// What a workspace starts on, and what the fp32 hidden planes need: their
+// stores are 32 bytes wide.
+constexpr size_t kWsAlign = 16, kHidAlign = 32;
+
 // Where everything lies in the workspace, a function of the descriptor alone.
 struct Layout {
   bool few;                  // forward of a few positions: hnd_ffn_few.cuh, operands token-major
@@ -185,6 +189,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
   l.pitch = l.token ? a.C : up(T, 8);
   l.hpitch = a.bf16 ? a.F : up(a.F, 16);      // fp32: whole 32-byte stores
   const bool copied = l.packed || !a.bf16;
+  // offsets are from the workspace rounded up to kHidAlign bytes (Ffn::ws)
   size_t at = 0;
   auto take = [&](long long elements, size_t size) {
     const size_t here = at;
@@ -217,7 +222,7 @@ static Layout layout(const FfnArgs& a, bool backward) {
     l.splits = static_cast<int>(cdiv(stages, per));
     if (l.splits > 1) l.part = take(3 * l.splits * l.w_plane, 4);
   }
-  l.bytes = at;
+  l.bytes = at + (a.bf16 ? 0 : kHidAlign - kWsAlign);
   return l;
 }
 
@@ -360,7 +365,10 @@ struct Ffn {
   const long long T;
   Mat x, dy, wg, wu, wd, hid[3];
 
-  char* ws(size_t at) const { return static_cast<char*>(a.ws) + at; }
+  char* ws(size_t at) const {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.ws);
+    return reinterpret_cast<char*>(F32 ? (base + kHidAlign - 1) / kHidAlign * kHidAlign : base) + at;
+  }
   bf16* wsb(size_t at) const { return reinterpret_cast<bf16*>(ws(at)); }
 
   Ffn(const FfnArgs& args, bool backward) : a(args), l(layout(args, backward)), T(args.B * args.L) {

@@ -242,6 +242,17 @@ def test_ffn_refusals():
     assert bwd(dwg=_ptr(1)) == H.ERR_INVALID_ARG and bwd(dwu=_ptr(6)) == H.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("B,C,L,F", [(40, 24, 1, 2088), (2, 64, 1024, 136), (5, 72, 37, 40), (1, 8, 1, 8)])
+def test_ffn_workspace_has_room_for_32_byte_stores(B, C, L, F):
+    """A workspace starts on 16 bytes; the fp32 hidden planes, which leave in stores of 32, start on the next 32
+    from there.  All parts are multiples of 256 bytes, so what is above a multiple is the room for that: 16 bytes or
+    more in each fp32 call that has such planes (up to 32 positions forward: none)."""
+    lib, f = K.load(), _ffn(B, C, L, F, dt=0)
+    for backward in (0, 1):
+        if backward or B * L > 32:
+            assert lib.hyena_nd_ffn_workspace_bytes(ctypes.byref(f), backward) % 256 >= 16
+
+
 def test_wrapper_refusals():
     import torch
 

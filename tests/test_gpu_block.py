@@ -499,6 +499,48 @@ def test_ffn_nan_stays_in_its_position(dims):
     assert not bad.any()
 
 
+@pytest.mark.parametrize("dims,B,C,F,dt", [((1,), 40, 24, 2088, "f32"), ((1,), 3, 24, 40, "f32"),
+                                           ((8, 8), 2, 64, 136, "f32"), ((37,), 3, 40, 72, "f32"),
+                                           ((37,), 3, 40, 72, "bf16"), ((8, 8), 2, 64, 136, "bf16"),
+                                           ((1,), 3, 24, 40, "bf16"), ((1,), 40, 24, 2088, "bf16")])
+def test_ffn_pointers_on_16_bytes(dims, B, C, F, dt):
+    """Every buffer of the C calls at 16 modulo 32, the least they ask for: the results are those of torch's own
+    buffers, and nothing beside a buffer changes, the workspace's exact size included."""
+    import ctypes
+
+    t = torch()
+    c = FfnCase(dims, B, C, F, dt, "gelu")
+    want_y, want_g = c.run()
+    held = []
+
+    def room(nbytes):
+        """nbytes at 16 modulo 32, in the middle of a buffer of sevens."""
+        buf = t.full((nbytes + 512,), 7, dtype=t.uint8, device="cuda")
+        at = 128 + (16 - buf.data_ptr()) % 32
+        assert (buf.data_ptr() + at) % 32 == 16
+        held.append((buf, at, nbytes))
+        return buf[at:at + nbytes]
+
+    def placed(v):
+        r = room(v.numel() * v.element_size())
+        r.copy_(v.reshape(-1).view(t.uint8))
+        return r
+
+    ins = [placed(c.t[k]) for k in ("x", "wg", "wu", "wd")]
+    dy, control = placed(c.t["dy"]), placed(t.zeros(256, dtype=t.uint8, device="cuda"))
+    y, *g = (room(v.numel() * v.element_size()) for v in (want_y, *want_g))
+    stream, f = t.cuda.current_stream().cuda_stream, ctypes.byref(c.op.f)
+    need = c.op.ws_bytes
+    ptr = lambda *v: [b.data_ptr() for b in v]  # noqa: E731
+    assert K.load().hyena_nd_ffn_forward(f, *ptr(*ins, y, control, room(need[0])), need[0], stream) == H.OK
+    assert K.load().hyena_nd_ffn_backward(f, *ptr(*ins, dy, *g, control, room(need[1])), need[1], stream) == H.OK
+    assert H.device_status(control.data_ptr(), stream) == H.OK
+    for got, want in zip((y, *g), (want_y, *want_g)):
+        assert t.equal(got.view(want.dtype), want.reshape(-1))
+    for buf, at, n in held:
+        assert (buf[:at] == 7).all() and (buf[at + n:] == 7).all()
+
+
 # ------------------------------------------------------- streams and graphs
 def test_two_streams_share_an_object():
     t = torch()

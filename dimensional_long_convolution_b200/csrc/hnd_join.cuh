@@ -401,8 +401,10 @@ __global__ void __launch_bounds__(kJoinMaxThreads)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int q = TL::slot(v);
-        const float yh = (raw_at(ry[k], v) - mu1[q]) * rho1[q];
-        const float md = (keep[k] >> v & 1u) ? hv[k][v] * j.factor : 0.f;
+        // a dropped value reaches no sum, whatever it is: 0 times an infinity would
+        const bool kept = keep[k] >> v & 1u;
+        const float yh = kept ? (raw_at(ry[k], v) - mu1[q]) * rho1[q] : 0.f;
+        const float md = kept ? hv[k][v] * j.factor : 0.f;
         if (TOK) {
           if (dgate) *HND_G(dgate + t.b * j.C + t.chan(k) + v) = z1[v] * md * (w1[v] * yh + b1[v]);
           acc[k][HND_PV(v)].x += gt[v] * md * yh;

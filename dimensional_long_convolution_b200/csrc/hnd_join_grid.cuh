@@ -653,7 +653,8 @@ __global__ void __launch_bounds__(kT, 2)
         float2 a = both(0.f), r = both(0.f);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-          const float2 yh = mul(add(Vec<TT>::get(ry, q), neg1[q]), rho1[q]);
+          // a dropped value reaches no sum, whatever it is: 0 times an infinity would
+          const float2 yh = G::kept(bits, q, mul(add(Vec<TT>::get(ry, q), neg1[q]), rho1[q]));
           const float2 md = G::kept(bits, q, mul(hv[k][q], both(j.factor)));
           a = fma(md, yh, a);
           r = add(r, md);

@@ -244,6 +244,26 @@ def test_join_drops_infinities_and_nan(dims):
     assert np.isinf(got[0, 0, 0]) == (c.m[0, 0, 0] > 0)
 
 
+@pytest.mark.parametrize("pre", ["none", "layer"])
+@pytest.mark.parametrize("dims,B,C,dt", [((1,), 4, 40, "f32"), ((1,), 400, 96, "bf16"), ((1,), 3, 33, "f32"),
+                                         ((16,), 4, 40, "f32"), ((64,), 2, 70, "bf16"), ((7,), 4, 40, "bf16"),
+                                         ((13,), 2, 40, "f32"), ((24,), 2, 700, "bf16"), ((9,), 2, 1100, "f32"),
+                                         ((8,), 1, 9000, "f32")])
+def test_join_gradients_drop_infinities_and_nan(dims, B, C, dt, pre):
+    """A dropped value of y reaches nothing, so the gradients (those of gate and scale sum over products with y) are
+    the ones of any finite value in its place."""
+    c = JoinCase(dims, B, C, dt, "none", pre, "wbgs", 0.5)
+    gone = np.argwhere(c.m == 0)
+    flat = c.t["y"].view(c.B, c.C, -1)
+    for k, value in enumerate((float("nan"), float("inf"), -float("inf"))):
+        i = torch().from_numpy(np.ascontiguousarray(gone[k::3].T)).cuda()
+        flat[i[0], i[1], i[2]] = value
+    c.v["y"][c.m == 0] = 0
+    c.check_forward()
+    got = c.check_backward()
+    assert (host(got["dy"], B, C)[c.m == 0] == 0).all()
+
+
 def test_join_nan_stays_in_its_position():
     for dims in ((16,), (7,), (1,)):
         c = JoinCase(dims, 3, 40, "f32", "layer", "rms", "wb", 0.0)

@@ -508,6 +508,48 @@ def test_ffn_gates_of_any_size(dims, dt, gate):
     assert (np.abs(dwg - want) <= 2.0 ** -22 * want).all()
 
 
+def _single_gates(dims, dt, kind, gates, act, slope, slopes, tol):
+    """One gate a hidden channel, u = 2^13, Wd the unit matrix: every result but dx is a single term of the formula at
+    each position.  act and its slope at the gates, magnitudes of the slope's terms, tol relative to the terms."""
+    C = F = gates.size
+    L, u = int(np.prod(dims)), 2.0 ** 13
+    x = np.zeros((1, C) + dims)
+    x[:, 0] = 1
+    wg, wu = np.zeros((F, C)), np.zeros((F, C))
+    wg[:, 0], wu[:, 0] = gates, u
+    x, wg, wu, wd, dy = (dev(v, dt) for v in (x, wg, wu, np.eye(C), np.ones((1, C) + dims)))
+    op = K.GatedFFN(dims, 1, C, F, io_dtype=dt, act=kind)
+    y = host(op(x, wg, wu, wd), 1, C)
+    dx, dwg, dwu, dwd = (host(v) for v in op.backward(x, wg, wu, wd, dy))
+    assert op.status() == H.OK
+    for name, got, want, mag in (("y", y[0].T, act * u, act * u), ("dwg", dwg[:, 0], slope * u * L, slopes * u * L),
+                                 ("dwu", dwu[:, 0], act * L, act * L), ("dwd", np.diag(dwd), act * u * L, act * u * L)):
+        off = np.abs(got - want) / np.abs(mag)
+        assert (off <= tol * 1.001).all(), (name, off / tol)
+    # the first channel's dx sums over the hidden channels
+    want, mag = gates * slope * u + u * act, np.abs(gates) * slopes * u + np.abs(u * act)
+    assert (np.abs(dx[0, 0] - want.sum()) <= (tol * mag).sum() + HALF_STEP[dt] * 1.001 * abs(want.sum())).all()
+
+
+SINGLE = [((1,), "bf16"), ((40,), "bf16"), ((1,), "f32"), ((40,), "f32")]
+
+
+@pytest.mark.parametrize("dims,dt", SINGLE)
+def test_ffn_gelu_far_below_zero(dims, dt):
+    """gelu(g) = g Phi(g) keeps its relative accuracy where Phi(g) is small, as g u may be large.  With bf16 the
+    hidden value and the stored result are rounded, half a step each, and Phi is good to 2^-13; fp32 functions are off
+    by a few steps, an argument by 2^-23, which moves exp(-g^2/2) by g^2 2^-23 of itself; 40 more steps of 2^-24 for
+    the sums of planes and of the positions.  The slope is a difference above -0.75: its tolerance is relative to both
+    terms."""
+    import math
+
+    gates = host(dev(np.linspace(-12.5, 12.5, 64), "bf16"))
+    phi = np.array([0.5 * math.erfc(-g / math.sqrt(2)) for g in gates])
+    bell = gates * np.exp(-0.5 * gates ** 2) / math.sqrt(2 * math.pi)
+    tol = (2 * HALF_STEP["bf16"] + 2.0 ** -13 if dt == "bf16" else 0) + (gates ** 2 + 40) * 2.0 ** -23
+    _single_gates(dims, dt, "gelu", gates, gates * phi, phi + bell, phi + np.abs(bell), tol)
+
+
 @pytest.mark.parametrize("dims", [(1,), (40,), (7,)])
 def test_ffn_nan_stays_in_its_position(dims):
     c = FfnCase(dims, 3, 64, 96, "bf16", "silu")

@@ -304,24 +304,30 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// 1 / (1 + exp(-g)) of two gates.  bf16: one reciprocal of the product serves
+// 1 / (1 + exp(-g)) of two gates, from w = exp(-|g|) <= 1: 1 / (1 + w) above
+// zero and w / (1 + w) below, which keeps its relative accuracy down to the
+// smallest normal number (g s u may be large all the same) and is 0 beyond.
+// bf16: one reciprocal of the product of the denominators, 4 at most, serves
 // both, since the special-function unit (two exponentials and two reciprocals
-// for a pair otherwise) is what the epilogue waits for; exp(-g) is held at
-// 2^60 to keep the product finite, and gates beyond that (-41.6) get 0, since
-// what is small next to 1 is not small once a large gate multiplies it.  fp32:
-// the reciprocal of an infinite exponential is 0 by itself.
+// for a pair otherwise) is what the epilogue waits for.  A NaN comes back as
+// 1/2, so that the other gate keeps its value, and is one again in the product
+// with g.
 template <bool F32>
 __device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
   if constexpr (F32) {
-    s[0] = recip_fast(1.f + expf(-g[0]));     // off by one unit in the last place at most
-    s[1] = recip_fast(1.f + expf(-g[1]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float w = expf(-fabsf(g[i])), r = recip_fast(1.f + w);     // off by one unit in the last place at most
+      s[i] = g[i] < 0.f ? w * r : r;
+    }
   } else {
-    float x[2];
+    float x[2], w[2];
     unpair(mul2(pair64(g[0], g[1]), pair64(-kLog2e, -kLog2e)), x);
-    const float d0 = 1.f + exp2_fast(fminf(x[0], 60.f)), d1 = 1.f + exp2_fast(fminf(x[1], 60.f));
-    const float r = recip_fast(d0 * d1);
-    s[0] = x[0] > 60.f ? 0.f : r * d1;
-    s[1] = x[1] > 60.f ? 0.f : r * d0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = exp2_fast(fminf(-fabsf(x[i]), 0.f));
+    const float d0 = 1.f + w[0], d1 = 1.f + w[1], r = recip_fast(d0 * d1), t[2] = {r * d1, r * d0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s[i] = g[i] < 0.f ? w[i] * t[i] : t[i];
   }
 }
 

@@ -550,6 +550,17 @@ def test_ffn_gelu_far_below_zero(dims, dt):
     _single_gates(dims, dt, "gelu", gates, gates * phi, phi + bell, phi + np.abs(bell), tol)
 
 
+@pytest.mark.parametrize("dims,dt", SINGLE)
+def test_ffn_silu_far_below_zero(dims, dt):
+    """silu(g) = g s, s = 1 / (1 + exp(-g)), keeps its relative accuracy where s is small.  Roundings as above; the
+    exponential's argument is off by 2^-23 of itself."""
+    gates = host(dev(np.linspace(-60.0, 60.0, 64), "bf16"))
+    s = 1.0 / (1.0 + np.exp(-gates))
+    bend = gates * s * (1.0 / (1.0 + np.exp(gates)))
+    tol = (2 * HALF_STEP["bf16"] if dt == "bf16" else 0) + (np.abs(gates) + 40) * 2.0 ** -23
+    _single_gates(dims, dt, "silu", gates, gates * s, s + bend, s + np.abs(bend), tol)
+
+
 @pytest.mark.parametrize("dims", [(1,), (40,), (7,)])
 def test_ffn_nan_stays_in_its_position(dims):
     c = FfnCase(dims, 3, 64, 96, "bf16", "silu")

@@ -321,6 +321,12 @@ class GatedFFN(_GridOp):
         if 0 in self.ws_bytes:
             raise H.HyenaNDError(H.ERR_UNSUPPORTED, "ffn_workspace_bytes")
         self.control = self.torch.zeros(256, dtype=self.torch.uint8, device=self.device)
+        if self.device.type == "cuda":
+            # no caller could order another stream behind that, so it is done before the object is used; made inside
+            # a capture, the object is for the graph's own stream and is cleared by each replay
+            with self.torch.cuda.device(self.device):
+                if not self.torch.cuda.is_current_stream_capturing():
+                    self.torch.cuda.current_stream().synchronize()
         self.fref = ctypes.byref(self.f)
         self.up, self.down = self.torch.Size((self.F, self.C)), self.torch.Size((self.C, self.F))
 
@@ -346,7 +352,9 @@ class GatedFFN(_GridOp):
         return out
 
     def status(self) -> int:
-        """Waits for the current stream, then reads and clears the device-side status."""
+        """Waits for the current stream, then reads and clears the device-side
+        status: that of the calls which the current stream comes after.  A call
+        still running on another stream may record one later."""
         stream = self._stream()
         with self.torch.cuda.device(self.device):
             return H.device_status(self.control.data_ptr(), stream)

@@ -615,6 +615,26 @@ def test_ffn_pointers_on_16_bytes(dims, B, C, F, dt):
 
 
 # ------------------------------------------------------- streams and graphs
+def test_ffn_control_is_set_up_before_the_object_is_used():
+    """The status word is cleared by the time the constructor returns: a code that a call on another stream records
+    stays, however late the constructing stream gets to its work."""
+    t = torch()
+    late, other = t.cuda.Stream(), t.cuda.Stream()
+    with t.cuda.stream(late):      # memory and kernels are there: nothing below waits for either
+        t.zeros(256, dtype=t.uint8, device="cuda")
+        t.zeros(64, dtype=t.int32, device="cuda")[0].fill_(H.ERR_DEVICE_TIMEOUT)
+        t.cuda._sleep(1)
+    t.cuda.synchronize()
+    with t.cuda.stream(late):
+        t.cuda._sleep(100_000_000)          # some 50 ms
+        op = K.GatedFFN((8,), 1, 8, 8)
+    with t.cuda.stream(other):
+        op.control.view(t.int32)[0].fill_(H.ERR_DEVICE_TIMEOUT)      # as a kernel would
+    t.cuda.synchronize()
+    assert op.status() == H.ERR_DEVICE_TIMEOUT
+    assert op.status() == H.OK               # read and cleared
+
+
 def test_two_streams_share_an_object():
     t = torch()
     c = FfnCase((32, 32), 2, 64, 256, "bf16", "silu")

@@ -137,7 +137,28 @@ hyena_nd_status join_backward(const hyena_nd_block_shape* s, hnd::JoinArgs& a, v
 
 }  // namespace
 
+#ifdef HYENA_ND_BOUNDS
+// Reads one byte through the check.
+static __global__ void k_bounds_probe(const unsigned char* p, unsigned char* out) { *HND_G(out) = *HND_G(p); }
+#endif
+
 extern "C" {
+
+#ifdef HYENA_ND_BOUNDS
+// For the tests of the checked build, which alone has it: registers the first
+// `registered` bytes of `buffer` and the byte `out` without a status word, and
+// reads byte `at` of the buffer, which has to be the caller's memory.
+HYENA_ND_API hyena_nd_status hyena_nd_debug_bounds_probe(const void* buffer, size_t registered, size_t at, void* out,
+                                                         void* cuda_stream) {
+  return guarded([&] {
+    const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    const hyena_nd_status st = bounds({{buffer, registered}, {out, 1}}, nullptr, stream);
+    if (st != HYENA_ND_OK) return st;
+    k_bounds_probe<<<1, 1, 0, stream>>>(static_cast<const unsigned char*>(buffer) + at, static_cast<unsigned char*>(out));
+    return cuda_status(cudaGetLastError());
+  });
+}
+#endif
 
 hyena_nd_status hyena_nd_norm_forward(const hyena_nd_block_shape* s, const hyena_nd_norm* norm, const void* x, void* n,
                                       void* cuda_stream) {

@@ -95,7 +95,9 @@ struct BoundsList {
   }
 };
 // Upload the list (and the status word to record in) for the kernels the
-// call is about to enqueue on `st`.  Normal build: does nothing.
+// call is about to enqueue on `st`.  A call without a status word of its own
+// (null) records in the library's, which hyena_nd_device_status reads for a
+// null workspace.  Normal build: does nothing.
 cudaError_t bounds_register(const BoundsList& list, int* status, cudaStream_t st);
 
 }  // namespace hnd

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(DUAL ? 256 : 512) k_ffn_few(const FewParams p)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)      // rows g and g + 8, positions 2 q and 2 q + 1
-        red[((warp * MATS + m) * NT * 8 + n * 8 + 2 * q + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
+        *HND_S(red + ((warp * MATS + m) * NT * 8 + n * 8 + 2 * q + (i & 1)) * 16 + g + 8 * (i >> 1)) = acc[m][n][i];
   __syncthreads();
   for (int i = threadIdx.x; i < NT * 128; i += blockDim.x) {
     const int t = i / 16, row = row0 + i % 16;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(DUAL ? 256 : 512) k_ffn_few(const FewParams p)
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
       s[m] = 0.f;
-      for (int v = 0; v < warps; ++v) s[m] += red[(v * MATS + m) * NT * 128 + i];
+      for (int v = 0; v < warps; ++v) s[m] += *HND_S(red + (v * MATS + m) * NT * 128 + i);
     }
     if constexpr (DUAL) {
       const float gv[2] = {s[0], s[0]}, uv[2] = {s[1], s[1]};

@@ -144,7 +144,7 @@ struct Tile {
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < P; ++i) out[(n * P + i) * sets] = s[n][i];
+        for (int i = 0; i < P; ++i) *HND_S(out + (n * P + i) * sets) = s[n][i];
     __syncthreads();
     const int from = TOK ? warp / (lanes / 32) * (lanes / 32) : 0, to = TOK ? from + lanes / 32 : warps;
 #pragma unroll
@@ -156,7 +156,7 @@ struct Tile {
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < P; ++i) s[n][i] += in[(n * P + i) * sets];
+        for (int i = 0; i < P; ++i) s[n][i] += *HND_S(in + (n * P + i) * sets);
     }
     flip ^= 1;      // the next sums go to the other half: no second barrier
   }

@@ -12,6 +12,8 @@
 
 #include <stdint.h>
 
+#include "hnd_bounds.cuh"
+
 namespace hnd {
 
 __device__ __forceinline__ uint4 philox10(uint4 c, uint32_t k0, uint32_t k1) {
@@ -32,7 +34,7 @@ struct DropState {
 };
 
 __device__ __forceinline__ DropState drop_state(const int64_t* rng) {
-  const uint64_t seed = static_cast<uint64_t>(rng[0]), off = static_cast<uint64_t>(rng[1]);
+  const uint64_t seed = static_cast<uint64_t>(*HND_G(rng)), off = static_cast<uint64_t>(*HND_G(rng + 1));
   return {static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(off),
           static_cast<uint32_t>(off >> 32)};
 }

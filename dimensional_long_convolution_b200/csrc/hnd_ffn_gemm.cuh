@@ -335,19 +335,18 @@ __device__ __forceinline__ void sigmoid2(const float (&g)[2], float (&s)[2]) {
 // the slope needs too.  Below zero Phi keeps its relative accuracy (1/2 +
 // erf/2 loses all of it from -5 on, and g Phi(g) u may be large all the same):
 // Phi(-z) = e M(z), where M falls slowly from 1/2 like 1 / (z sqrt(2 pi)), and
-// M = t P(t) in t = 1 / (1 + a z), P fitted over 0 <= z <= 16 for the least
+// M = t P(t) in t = 1 / (1 + 0.35 z), P fitted over 0 <= z <= 16 for the least
 // greatest relative error (a linear program on M = erfcx(z / sqrt 2) / 2):
-// degree 4 and 7.2e-5 for bf16, degree 8 and 3.2e-8 for fp32.  Beyond 16, e is
-// 0 in fp32, so that z may be cut at 64, which keeps z^2 and the product of
-// both denominators finite; one reciprocal serves both gates.  A NaN comes
-// back as 1 and is one again in the product with g.
+// 3.2e-8 at degree 8.  bf16 takes it too, since the slope crosses zero at
+// -0.75 and would keep an absolute error there (degree 4 has 7.2e-5).  Beyond
+// 16, e is 0 in fp32, so that z may be cut at 64, which keeps z^2 and the
+// product of both denominators finite; one reciprocal serves both gates.  A
+// NaN comes back as 1 and is one again in the product with g.
 template <bool F32>
 __device__ __forceinline__ void normal2(const float (&g)[2], float (&cdf)[2], float (&e)[2]) {
-  constexpr float a = F32 ? 0.35f : 0.25f;
-  constexpr int N = F32 ? 9 : 5;
-  constexpr float c32[9] = {0.139621243f,  0.139864534f, 0.11981415f,  0.105579965f,  -0.0232757367f,
-                            0.159409821f, -0.255916387f, 0.14406772f, -0.0291653275f};
-  constexpr float c16[5] = {0.101065211f, 0.0828303397f, 0.173842475f, -0.0961801559f, 0.238406241f};
+  constexpr float a = 0.35f;
+  constexpr float c[9] = {0.139621243f, 0.139864534f,  0.11981415f, 0.105579965f,  -0.0232757367f,
+                          0.159409821f, -0.255916387f, 0.14406772f, -0.0291653275f};
   float z[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -363,9 +362,9 @@ __device__ __forceinline__ void normal2(const float (&g)[2], float (&cdf)[2], fl
   const float t[2] = {r * d1, r * d0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float q = F32 ? c32[8] : c16[4];
+    float q = c[8];
 #pragma unroll
-    for (int k = N - 2; k >= 0; --k) q = fmaf(q, t[i], F32 ? c32[k] : c16[k < 5 ? k : 0]);
+    for (int k = 7; k >= 0; --k) q = fmaf(q, t[i], c[k]);
     q *= t[i] * e[i];
     cdf[i] = g[i] < 0.f ? q : 1.f - q;
   }

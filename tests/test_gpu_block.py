@@ -550,6 +550,30 @@ def test_ffn_gelu_far_below_zero(dims, dt):
     _single_gates(dims, dt, "gelu", gates, gates * phi, phi + bell, phi + np.abs(bell), tol)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dims", [(1,), (33,)])
+def test_ffn_gelu_where_its_slope_is_zero(dims, dt):
+    """gelu's slope crosses zero near -0.7518: what its error is there, is to the terms of Phi + g phi no more than
+    elsewhere.  One gate a hidden channel around the crossing, one for all positions."""
+    import math
+
+    gates = host(dev(np.linspace(-0.8, -0.7, 64), dt))
+    phi = np.array([0.5 * math.erfc(-g / math.sqrt(2)) for g in gates])
+    bell = gates * np.exp(-0.5 * gates ** 2) / math.sqrt(2 * math.pi)
+    C = F = gates.size
+    x = np.zeros((1, C) + dims)
+    x[:, 0] = 1
+    wg, wu = np.zeros((F, C)), np.zeros((F, C))
+    wg[:, 0], wu[:, 0] = gates, 1
+    x, wg, wu, wd, dy = (dev(v, dt) for v in (x, wg, wu, np.eye(C), np.ones((1, C) + dims)))
+    got = host(K.GatedFFN(dims, 1, C, F, io_dtype=dt, act="gelu").backward(x, wg, wu, wd, dy)[1])[:, 0]
+    L, want = int(np.prod(dims)), phi + bell
+    # the slope and its sum over L equal terms are rounded, each half a step of itself (bf16); 16 steps of 2^-24 of the
+    # slope's terms and L / 8 + 16 of the sum's for the arithmetic
+    tol = (2 * HALF_STEP[dt] * 1.01 + (L / 8 + 16) * 2.0 ** -24) * np.abs(want) + 16 * 2.0 ** -24 * (phi - bell)
+    assert (np.abs(got / L - want) <= tol).all(), np.abs(got / L - want) / tol
+
+
 @pytest.mark.parametrize("dims,dt", SINGLE)
 def test_ffn_silu_far_below_zero(dims, dt):
     """silu(g) = g s, s = 1 / (1 + exp(-g)), keeps its relative accuracy where s is small.  Roundings as above; the

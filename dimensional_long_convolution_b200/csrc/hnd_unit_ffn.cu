@@ -157,6 +157,15 @@ static int data_splits(long long tiles, long long stages) {
   return static_cast<int>(cdiv(stages, cdiv(stages, s)));
 }
 
+// The most stages that one accumulator of a bf16 product adds up.  The tensor
+// core cuts what it adds to an accumulator, always towards zero (fp32: see
+// Params::piece), and over T positions the loss grows with T: sums of equal
+// signs were off by 1.0e-3 at 9362 additions, 4.2e-3 at 43690, more than the
+// result's own rounding.  4096 additions, 4 a stage, lose 4.5e-4; the other
+// products' depth, 65536 channels at most, comes to the same.  (2^20 positions,
+// C 256, F 1024: 6 splits, 16 so, training 7.55 -> 7.67 ms.)
+constexpr long long kDeepest = 1024;
+
 // Splits of the weight gradients' K loops.  In stages of a pair (0.27 us at
 // full rate): rounds of tiles, each with 8 stages' worth for a tile's ends;
 // split, the partial sums go through memory once each way and one more
@@ -218,7 +227,8 @@ static Layout layout(const FfnArgs& a, bool backward) {
   if (backward) {
     // every split gets a stage at least
     const long long stages = l.batches * cdiv(l.Lx, kBK);
-    const long long per = cdiv(stages, weight_splits(a.C, a.F, stages * (a.bf16 ? 1 : 6)));
+    long long per = cdiv(stages, weight_splits(a.C, a.F, stages * (a.bf16 ? 1 : 6)));
+    if (a.bf16 && per > kDeepest) per = kDeepest;
     l.splits = static_cast<int>(cdiv(stages, per));
     if (l.splits > 1) l.part = take(3 * l.splits * l.w_plane, 4);
   }

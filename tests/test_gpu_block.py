@@ -585,6 +585,35 @@ def test_ffn_silu_far_below_zero(dims, dt):
     _single_gates(dims, dt, "silu", gates, gates * s, s + bend, s + np.abs(bend), tol)
 
 
+def test_ffn_weight_gradients_over_a_million_positions():
+    """The tensor cores cut what they add to an accumulator, which is off by as much as 2^-23 of the sum an addition
+    and always the same way; no loop may be so deep that this shows next to bf16's 2^-8.  Gates of 64, where silu is
+    the gate itself and its slope 1, one channel of x that is 1 and one row of Wd: the gradients are 2^20 equal terms,
+    known exactly.  A sum that grows evenly loses half of 2^-23 an addition: 2^-12 in 4096, the most of a loop, and
+    2^-11 on average is allowed for a product of 16 that is added in two steps."""
+    t = torch()
+    C, F, L = 1024, 1536, 1 << 20
+    if t.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB of device memory")
+    r = np.random.default_rng(4)
+    u, d = (host(dev(1 + r.random(n), "bf16")) for n in (F, C))
+    wg, wu, wd = np.zeros((F, C)), np.zeros((F, C)), np.zeros((C, F))
+    wg[:, 0], wu[:, 0], wd[0] = 64, u, 1
+    x = t.zeros(1, C, L, dtype=t.bfloat16, device="cuda")
+    x[:, 0] = 1
+    dy = dev(d, "bf16").view(1, C, 1).expand(1, C, L).contiguous()
+    op = K.GatedFFN((L,), 1, C, F, io_dtype="bf16", act="silu")
+    _, dwg, dwu, dwd = op.backward(x, *(dev(v, "bf16") for v in (wg, wu, wd)), dy)
+    assert op.status() == H.OK
+    stored = lambda v: host(dev(v, "bf16"))  # noqa: E731  (one rounding of exact products of 16 bits)
+    for name, got, want in (("dwg", dwg[:, 0], stored(d[0] * u) * L), ("dwu", dwu[:, 0], stored(np.full(F, 64 * d[0])) * L),
+                            ("dwd", dwd, 64.0 * L * d[:, None] * u[None, :])):
+        off = host(got) / want - 1
+        assert np.abs(off).max() <= HALF_STEP["bf16"] * 1.01 + 2.0 ** -12, (name, off.min(), off.max())
+        if name == "dwd":
+            assert abs(off.mean()) <= 2.0 ** -11, off.mean()
+
+
 @pytest.mark.parametrize("dims", [(1,), (40,), (7,)])
 def test_ffn_nan_stays_in_its_position(dims):
     c = FfnCase(dims, 3, 64, 96, "bf16", "silu")

@@ -614,6 +614,38 @@ def test_ffn_weight_gradients_over_a_million_positions():
             assert abs(off.mean()) <= 2.0 ** -11, off.mean()
 
 
+@pytest.mark.parametrize("dims,B,C,F,dt", [(((1 << 28) + 8,), 1, 8, 16, "bf16"), (((1 << 27) + 5,), 2, 8, 16, "bf16"),
+                                           ((1,), (1 << 28) - 5, 8, 16, "bf16"), (((1 << 26) + 7,), 1, 8, 40, "f32")])
+def test_ffn_beyond_32_bits(dims, B, C, F, dt):
+    """Activations and hidden values past 2^31 elements: the last positions, against the oracle on them alone."""
+    t = torch()
+    t.cuda.empty_cache()
+    if t.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB of device memory")
+    c = FfnCase((40,), 1, C, F, dt, "silu")
+    w = [c.t[k] for k in ("wg", "wu", "wd")]
+    x, dy = (t.empty((B, C) + dims, dtype=c.t["x"].dtype, device="cuda").normal_() for _ in range(2))
+    op = K.GatedFFN(dims, B, C, F, io_dtype=dt)
+    y = op(x, *w)
+    n = 40 if dims != (1,) else 1
+
+    def tail(v):
+        return host(v[-1:, :, -n:] if n > 1 else v[-40:], 1 if n > 1 else 40, C)
+
+    V = c.v
+    q = O.ffn_terms(tail(x), V["wg"], V["wu"], V["wd"], tail(dy), "silu")
+    want = O.ffn(tail(x), V["wg"], V["wu"], V["wd"], "silu")
+    mag = O.uncols(np.abs(V["wd"]) @ np.abs(q["H"]), want.shape[0])
+    step = 3 * HALF_STEP[dt] + 2.0 ** -18          # hidden value, result; fp32 arithmetic of the planes
+    assert (np.abs(tail(y) - want) <= step * mag + 1e-37).all()
+    del y
+    dx = op.backward(x, *w, dy)[0]
+    assert op.status() == H.OK
+    want = O.ffn_backward(tail(x), V["wg"], V["wu"], V["wd"], tail(dy), "silu")[0]
+    mag = np.abs(V["wg"]).T @ (np.abs(q["DH"] * q["U"]) * 1.2) + np.abs(V["wu"]).T @ np.abs(q["DU"])
+    assert (np.abs(tail(dx) - want) <= step * O.uncols(mag, want.shape[0]) + 1e-37).all()
+
+
 @pytest.mark.parametrize("dims", [(1,), (40,), (7,)])
 def test_ffn_nan_stays_in_its_position(dims):
     c = FfnCase(dims, 3, 64, 96, "bf16", "silu")

@@ -97,8 +97,7 @@ struct Params {
   CUtensorMap map[kMaxMaps];
   Seg seg[kMaxSegs];
   Job job[kMaxJobs];
-  int jobs, tiles;
-  int planes;                // 1, or 3 for fp32
+  int tiles;
   int a_plane, b_plane;      // third-coordinate distance of the planes
   int act;
   int piece;                 // fp32: stages of each segment that the tensor core adds up

@@ -115,7 +115,9 @@ __global__ void __launch_bounds__(256)
 static long long up(long long v, long long a) { return (v + a - 1) / a * a; }
 static long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
-constexpr int kPairs = 74;   // CTA pairs of a B200
+// CTA pairs of a B200.  The layout counts with this constant, so that a
+// workspace's size is the descriptor's alone; launches ask the device.
+constexpr int kPairs = 74;
 
 // What a workspace starts on, and what the fp32 hidden planes need: their
 // stores are 32 bytes wide.
@@ -276,7 +278,7 @@ static bool encode(CUtensorMap* map, const Mat& m, int box_inner, int box_rows, 
 // -------------------------------------------------------------------- launch
 struct Launch {
   Params p{};
-  int maps = 0, segs = 0;
+  int maps = 0, jobs = 0;
   bool ok = true;
 
   int add(const Mat& m, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
@@ -294,14 +296,14 @@ struct Launch {
   int store_hidden(const Mat& m, int wide) {
     return add(m, wide, 128, wide == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   }
-  void job(const Job& j) { p.job[p.jobs++] = j; }
+  void job(const Job& j) { p.job[jobs++] = j; }
 };
 
 template <int EPI, bool F32>
 static cudaError_t run(Launch& l, cudaStream_t st) {
   if (!l.ok) return cudaErrorInvalidValue;
   long long tiles = 0;
-  for (int i = 0; i < l.p.jobs; ++i) {
+  for (int i = 0; i < l.jobs; ++i) {
     Job& j = l.p.job[i];
     const long long per = static_cast<long long>(j.batches) * j.mt * j.nt;
     tiles += per * j.splits;
@@ -430,7 +432,6 @@ struct Ffn {
 
   Launch start() const {
     Launch n;
-    n.p.planes = l.planes;
     n.p.act = a.act;
     n.p.piece = 4;
     n.p.status = a.status;
@@ -530,7 +531,7 @@ struct Ffn {
     if ((e = pack(true)) != cudaSuccess) return e;
     // H, dG, dU
     Launch h = start();
-        if (F32) {
+    if (F32) {
       h.p.seg[0] = gates_seg(h, gn, gn);
       h.p.seg[1] = data_seg(positions(h, dy), h.mn(wd), !l.token, true, gn, 2 * gn, 1);
     } else {      // dH of 256 channels, then G and U of 128 and of the other 128

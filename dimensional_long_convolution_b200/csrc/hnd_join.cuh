@@ -34,7 +34,7 @@ struct JoinDev {
   const int64_t* rng;
 };
 
-// The aligned-grid kernels of hnd_join_grid.cuh: K channels of a thread, w
+// The persistent kernels of hnd_join_grid.cuh: K channels of a thread, w
 // lanes of positions, and (gradients) `chunks` blocks a sample.
 cudaError_t launch_join_grid_fwd(const JoinArgs& a, const JoinDev& j, int w, int K, unsigned blocks);
 cudaError_t launch_join_grid_bwd(const JoinArgs& a, const JoinDev& j, int w, int K, int chunks, unsigned blocks,

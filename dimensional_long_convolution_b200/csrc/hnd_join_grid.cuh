@@ -1,5 +1,5 @@
-// hnd_join_grid.cuh -- the join on aligned grids: persistent blocks that bring
-// the next tile while they work on this one.
+// hnd_join_grid.cuh -- the join on grids: persistent blocks that bring the next
+// tile while they work on this one.
 //
 // What hnd_join.cuh does in registers alone is held back by its loads: a block
 // waits for its tile, works, stores, and the two blocks an SM has room for

@@ -4,9 +4,13 @@
 namespace hnd {
 
 // ----------------------------------------- any number of channels, any length
-// For more channels than a block of hnd_join.cuh holds in registers (4096
-// forward, 2048 in the gradients of grids): a block takes 32 positions and
-// reads their channels again for each of its sweeps, from L2 mostly.
+// For more channels than a block of hnd_join.cuh holds in registers: a block
+// takes 32 positions and reads their channels again for each of its sweeps,
+// from L2 mostly.  Such a block holds (join_plan), with rows of whole 16-byte
+// vectors, 16384 channels of a token forward and 8192 in the gradients, of a
+// grid's positions 4096 (fp32) or 2048 (bf16) forward and 2048 in the
+// gradients; with other rows 8192 and 4096 of a token, 16384 and 4096 of a
+// grid.
 constexpr int kJoinLanes = 32;   // positions of a block
 constexpr int kJoinRows = 8;     // channel rows of a block
 
@@ -299,8 +303,9 @@ static bool grid_plan(JoinPlan& p, long long C, long long units, int widest) {
   return false;
 }
 
-// Grids of up to 512 channels (fp32 forward 1024): as many lanes of positions
-// as leave threads for the channels, two at least where a row has two vectors.
+// Grids of up to 512 channels (fp32 forward 1024; more where there is but one
+// vector to a block): as many lanes of positions as leave threads for the channels, two
+// at least where a row has two vectors.
 static bool ahead_plan(JoinPlan& p, long long B, long long C, long long L, int bf16, bool backward) {
   const int V = bf16 ? 8 : 4, most = backward || bf16 ? 4 : 8;
   if (L == 1) return false;

@@ -1,4 +1,5 @@
-// Instantiations of the join on aligned grids.
+// Instantiations of the join's persistent kernels on grids, with rows of whole
+// vectors and ragged ones.
 #include "hnd_host_util.h"
 #include "hnd_join_grid.cuh"
 

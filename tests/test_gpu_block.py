@@ -181,6 +181,19 @@ def test_join_parity(dims, B, C, dt, post, pre, params, p):
     c.check_backward()
 
 
+@pytest.mark.parametrize("dims,C,dt", [
+    # the most channels of each kind of block, and one more: persistent, registers, any number
+    ((24,), 512, "bf16"), ((24,), 513, "bf16"), ((24,), 1024, "f32"), ((24,), 1025, "f32"), ((25,), 513, "f32"),
+    ((24,), 2048, "bf16"), ((24,), 2049, "bf16"), ((24,), 3000, "bf16"), ((24,), 4096, "f32"), ((24,), 4097, "f32"),
+    ((25,), 4096, "bf16"), ((25,), 4097, "f32"), ((25,), 16384, "bf16"), ((25,), 16385, "f32"),
+    ((1,), 4095, "bf16"), ((1,), 4097, "f32"), ((1,), 8192, "bf16"), ((1,), 8193, "f32"), ((1,), 8200, "bf16"),
+    ((1,), 16384, "f32"), ((1,), 16392, "bf16"), ((4,), 1024, "bf16"), ((3,), 2048, "f32"), ((3,), 2049, "f32")])
+def test_join_parity_at_the_limits_of_its_kernels(dims, C, dt):
+    c = JoinCase(dims, 2, C, dt, "layer", "rms", "wbgs", 0.1)
+    c.check_forward()
+    c.check_backward()
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("dims,C", [((13,), 24), ((8, 8), 64), ((777,), 9)])
 def test_join_writes_its_outputs_only(dims, C, dt):

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import Optional, Sequence
 
 from . import hyena_nd as H
@@ -95,6 +96,11 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+_CONTROL_BYTES = 256
+_controls: dict = {}        # of each device, cleared control words for new objects
+_control_lock = threading.Lock()
+
+
 # ------------------------------------------------------------ torch wrappers
 class _GridOp:
     """What the operators share: shape, device, argument checks, stream."""
@@ -158,6 +164,27 @@ class _GridOp:
         if rng is None:
             raise ValueError("dropout needs rng, an int64 tensor (seed, offset)")
         return self._check_param("rng", rng, (2,), self.torch.int64)
+
+    def _control_word(self):
+        """256 zero bytes that calls on any stream may use at once: no caller could order another stream behind
+        their clearing.  They come from a block that was cleared, and waited for, for many objects; where a capture
+        needs a new one, the bytes are the graph's own and are cleared by each replay."""
+        torch = self.torch
+
+        def zeros(n):
+            return torch.zeros(n * _CONTROL_BYTES, dtype=torch.uint8, device=self.device)
+
+        if self.device.type != "cuda":
+            return zeros(1)
+        with _control_lock:
+            left = _controls.setdefault(self.device.index, [])
+            if not left:
+                with torch.cuda.device(self.device):
+                    if torch.cuda.is_current_stream_capturing():
+                        return zeros(1)
+                    left.extend(zeros(64).split(_CONTROL_BYTES))
+                    torch.cuda.current_stream().synchronize()
+            return left.pop()
 
     def _scratch(self, nbytes: int):
         return self.torch.empty(max(nbytes, 16), dtype=self.torch.uint8, device=self.device)
@@ -320,13 +347,7 @@ class GatedFFN(_GridOp):
         self.ws_bytes = [int(self.lib.hyena_nd_ffn_workspace_bytes(ctypes.byref(self.f), k)) for k in (0, 1)]
         if 0 in self.ws_bytes:
             raise H.HyenaNDError(H.ERR_UNSUPPORTED, "ffn_workspace_bytes")
-        self.control = self.torch.zeros(256, dtype=self.torch.uint8, device=self.device)
-        if self.device.type == "cuda":
-            # no caller could order another stream behind that, so it is done before the object is used; made inside
-            # a capture, the object is for the graph's own stream and is cleared by each replay
-            with self.torch.cuda.device(self.device):
-                if not self.torch.cuda.is_current_stream_capturing():
-                    self.torch.cuda.current_stream().synchronize()
+        self.control = self._control_word()
         self.fref = ctypes.byref(self.f)
         self.up, self.down = self.torch.Size((self.F, self.C)), self.torch.Size((self.C, self.F))
 

@@ -24,8 +24,8 @@
 // next lane's first.  (One value a thread and load, as hnd_join.cuh does it for
 // such rows, took 107 us for 13 x 204 x 777 bf16 forward and backward, this 90.)
 //
-// 2 x 128 x 256^2 bf16 forward: 31 us.  8 x 256 x 64^2 fp32: forward 31 us,
-// backward 67, bound by instruction issue and latency (51 and 42% of the slots).
+// 2 x 128 x 256^2 bf16 forward: 31 us.  8 x 256 x 64^2 fp32: forward 32 us,
+// backward 67, bound by latency (51 and 42% of the issue slots).
 #pragma once
 
 #include "hnd_div.cuh"

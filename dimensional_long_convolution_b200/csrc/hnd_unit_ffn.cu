@@ -164,8 +164,9 @@ static int data_splits(long long tiles, long long stages) {
 // Params::piece), and over T positions the loss grows with T: sums of equal
 // signs were off by 1.0e-3 at 9362 additions, 4.2e-3 at 43690, more than the
 // result's own rounding.  4096 additions, 4 a stage, lose 4.5e-4; the other
-// products' depth, 65536 channels at most, comes to the same.  (2^20 positions,
-// C 256, F 1024: 6 splits, 16 so, training 7.55 -> 7.67 ms.)
+// products' depth, 65536 channels at most (dx: twice), comes to the same or
+// twice that.  (2^20 positions, C 256, F 1024: 6 splits before, 16 so, training
+// 7.55 -> 7.67 ms.)
 constexpr long long kDeepest = 1024;
 
 // Splits of the weight gradients' K loops.  In stages of a pair (0.27 us at

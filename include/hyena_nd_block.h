@@ -35,7 +35,7 @@ extern "C" {
 
 /* Activations [B, C, L]: L is the product of the grid's extents, any length
  * from 1 (single tokens) on; B, C >= 1, B C L < 2^40, C <= 65536,
- * B L < 2^31.  With L = 1 a position's channels lie next to each other, so
+ * B L < 2^31, B C < 2^31.  With L = 1 a position's channels lie next to each other, so
  * token-major [T, C] activations are B = T, L = 1. */
 typedef struct {
   int64_t B, C, L;
@@ -129,8 +129,11 @@ HYENA_ND_API hyena_nd_status hyena_nd_dropout(const hyena_nd_block_shape* s, dou
  * Weights in the activations' dtype, row-major: Wg, Wu [F, C], Wd [C, F].
  * C and F: multiples of 8 up to 65536 (else HYENA_ND_ERR_UNSUPPORTED).
  * With bf16 the hidden values act(g) u, and in the gradients those of g and u
- * too, are rounded to bf16 once before the next product.  With fp32 an
- * infinity in an operand gives NaN in what it reaches. */
+ * too, are rounded to bf16 once before the next product.  act and its slope
+ * keep their relative accuracy where they are small, down to the smallest
+ * normal number (the slope as a sum of its two terms).  With fp32 an infinity
+ * in an operand or a hidden value gives NaN in what it reaches, and values
+ * below 2^-110 are good to 2^-133. */
 typedef enum { HYENA_ND_ACT_SILU = 0, HYENA_ND_ACT_GELU = 1 } hyena_nd_act;
 
 typedef struct {

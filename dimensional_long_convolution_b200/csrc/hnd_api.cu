@@ -64,13 +64,9 @@ cudaError_t side_stream(SideStream** out) {
 
 #ifdef HYENA_ND_BOUNDS
 __device__ BoundsTable g_bounds;
-__device__ __align__(32) unsigned char g_bounds_dummy[256];
+__device__ __align__(16) unsigned char g_bounds_dummy[256];
 
 cudaError_t bounds_register(const BoundsList& l, int* status, cudaStream_t st) {
-  if (!status) {
-    const cudaError_t e = static_status_word(&status);
-    if (e != cudaSuccess) return e;
-  }
   BoundsTable t{};
   for (int i = 0; i < l.n; ++i) {
     t.base[i] = reinterpret_cast<unsigned long long>(l.ptr[i]);

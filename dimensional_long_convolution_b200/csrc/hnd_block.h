@@ -40,6 +40,12 @@ struct JoinArgs {
   cudaStream_t stream = nullptr;
 };
 
+// bounds_register for these operators: a call without a status word of its own
+// records in the library's, which hyena_nd_device_status reads for a null
+// workspace.
+struct BoundsList;
+cudaError_t register_buffers(const BoundsList& list, int* status, cudaStream_t st);
+
 cudaError_t launch_join_forward(const JoinArgs& a);
 cudaError_t launch_join_backward(const JoinArgs& a);
 size_t join_workspace(long long B, long long C, long long L, int bf16);

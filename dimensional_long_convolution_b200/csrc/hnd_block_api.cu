@@ -3,10 +3,25 @@
 #include "hyena_nd_block.h"
 #include "hnd_block.h"
 #include "hnd_bounds.cuh"
+#include "hnd_launch.h"
 
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+
+namespace hnd {
+
+cudaError_t register_buffers(const BoundsList& list, int* status, cudaStream_t st) {
+#ifdef HYENA_ND_BOUNDS
+  if (!status) {
+    const cudaError_t e = static_status_word(&status);
+    if (e != cudaSuccess) return e;
+  }
+#endif
+  return bounds_register(list, status, st);
+}
+
+}  // namespace hnd
 
 namespace {
 
@@ -84,7 +99,7 @@ hyena_nd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? HYENA_ND_
 hyena_nd_status bounds(std::initializer_list<Span> spans, int* status, cudaStream_t st) {
   hnd::BoundsList bl;
   for (const Span& s : spans) bl.add(s.p, s.bytes);
-  return cuda_status(hnd::bounds_register(bl, status, st));
+  return cuda_status(hnd::register_buffers(bl, status, st));
 }
 
 // Nothing thrown leaves a C entry.

@@ -35,7 +35,7 @@ struct BoundsTable {
 // One table for the whole library (relocatable device code), written by the
 // host at the start of every call (stream-ordered).
 extern __device__ BoundsTable g_bounds;
-extern __device__ __align__(32) unsigned char g_bounds_dummy[256];      // the widest access: 32 bytes
+extern __device__ __align__(16) unsigned char g_bounds_dummy[256];
 
 __device__ __forceinline__ bool bounds_ok(const void* p, size_t nbytes) {
   if (__isShared(p)) {
@@ -95,9 +95,7 @@ struct BoundsList {
   }
 };
 // Upload the list (and the status word to record in) for the kernels the
-// call is about to enqueue on `st`.  A call without a status word of its own
-// (null) records in the library's, which hyena_nd_device_status reads for a
-// null workspace.  Normal build: does nothing.
+// call is about to enqueue on `st`.  Normal build: does nothing.
 cudaError_t bounds_register(const BoundsList& list, int* status, cudaStream_t st);
 
 }  // namespace hnd

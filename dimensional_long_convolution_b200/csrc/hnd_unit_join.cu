@@ -430,7 +430,7 @@ static cudaError_t grads(const JoinArgs& a, const float4* part, long long rows, 
     bl.add(p, C4);
   bl.add(a.gate, BC4);
   bl.add(a.dgate, BC4);
-  const cudaError_t e = bounds_register(bl, nullptr, a.stream);
+  const cudaError_t e = register_buffers(bl, nullptr, a.stream);
   if (e != cudaSuccess) return e;
   k_join_grads<<<static_cast<unsigned>(wide * (a.dgate && per ? 1 + a.B : 1)), dim3(32, 32), 0, a.stream>>>(
       device_view(a), part, rows, per, JoinGradsDev{a.dpost_w, a.dpost_b, a.dgate, a.dscale, a.dpre_w, a.dpre_b});

@@ -752,6 +752,46 @@ def test_two_streams_share_an_object():
     assert all(t.equal(a, want1) and t.equal(b, want2) for a, b in got)
 
 
+def test_host_threads_share_objects():
+    """Two threads, each on a stream of its own and with a generator state of its own, call the same objects; another
+    object is made meanwhile in each."""
+    import threading
+
+    t = torch()
+    c = JoinCase((64,), 3, 72, "bf16", "rms", "layer", "wbgs", 0.3)
+    f = FfnCase((64,), 3, 72, 136, "f32", "gelu")
+    drop = K.GridDropout((64,), 3, 72, io_dtype="bf16", p=0.4)
+    w = [f.t[k] for k in ("wg", "wu", "wd")]
+    states = [rng_state(5, 6), rng_state(7, 8)]
+
+    def step(rng):
+        h, n = c.op(c.t["x"], c.t["y"], rng=rng)
+        g = c.op.backward(c.t["x"], c.t["y"], c.t["dh"], c.t["dn"], rng=rng)
+        own = K.GatedFFN((64,), 3, 72, 136, io_dtype="f32", act="gelu")
+        return [h, n, drop(n, rng)] + [g[k] for k in sorted(g)] + [f.op(f.t["x"], *w), own(f.t["x"], *w)] \
+            + list(f.op.backward(f.t["x"], *w, f.t["dy"]))
+
+    want = [step(s) for s in states]
+    t.cuda.synchronize()
+    wrong, done = [], []
+
+    def work(i):
+        with t.cuda.stream(t.cuda.Stream()):
+            for _ in range(20):
+                got = step(states[i])
+                t.cuda.current_stream().synchronize()
+                if not all(t.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+        done.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert sorted(done) == [0, 1] and not wrong and not t.equal(want[0][0], want[1][0]) and f.op.status() == H.OK
+
+
 def test_graphs_follow_the_generator_state():
     """A captured forward and backward replays with the state's new values;
     two graphs of one object do not share scratch."""
